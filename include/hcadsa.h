@@ -326,6 +326,118 @@ hcadsa_status attn_gate_vha_fwd(const hcadsa_bf16* O, const hcadsa_bf16* cq, con
                                 const float* V, hcadsa_bf16* Y, int B, int L, int H, int dv, int rq, int r,
                                 hcadsa_stream stream);
 
+/* ------------------------------------------------------------------ paged cache of the MLA layers */
+
+/*
+ * The full-context (MLA) layers' K/V cache in pages, for serving: ragged batches in which every
+ * sequence has its own length and chunk of new tokens, and caches held to a budget by evicting the
+ * rows that received the least attention.  Source: the mirrorspeed page, section "Hybrid sparse
+ * attention, 1/7 full context access" (the MLA layers keep every token; 256-wide heads).  The
+ * pages describe no serving cache; the layout is this library's.
+ *
+ * Common to the calls below:
+ *   K_pool, V_pool : [n_pages, page, Hkv, 256] bf16; consecutive pages lie k_page_stride /
+ *              v_page_stride elements apart (a multiple of 8, at least page * Hkv * 256), so K and V
+ *              may be halves of one pool.  A pool row belongs to one token and K/V head.
+ *   table   : [B, max_pages] int32; row i of sequence b's cache lies in page
+ *              table[b][i / page] at place i % page
+ *   cu_q    : [B + 1] int32, ascending; sequence b's new tokens are the packed rows cu_q[b] ..
+ *              cu_q[b+1]-1 (none, one, or a chunk).  Packed rows behind cu_q[B] are neither read nor
+ *              written.
+ *   kv_len  : [B] int32, rows in b's cache, its new tokens included
+ *   seen    : [B] int32, tokens the sequence has had, the new ones included (kv_len plus what was
+ *              evicted); NULL: kv_len
+ *   pos, mass : [n_pages, page, Hkv] int32 / fp32, position and accumulated attention weight of every
+ *              pool row
+ * page is a power of two, 16 to 1024; d == 256; Hq / Hkv a power of two up to 128 (HCADSA_ERR_
+ * UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and mass need 4-byte alignment (moves: 8),
+ * the bf16 tensors 16.  The lengths and tables are device data: a value out of range (a page that
+ * is not in the pool, a length beyond max_pages * page, cu_q out of order) is recorded as
+ * HCADSA_ERR_DEVICE_BOUNDS, and the rows it concerns are skipped or read as zeros; nothing outside
+ * the tensors is touched.
+ */
+
+/*
+ * Writes a chunk's new rows to the ends of their sequences' caches: packed row cu_q[b] + i becomes
+ * row kv_len[b] - n_b + i of sequence b (n_b its new tokens), with pos = seen[b] - n_b + i and
+ * mass = 0.
+ *   K, V : [T, Hkv, 256] bf16, consecutive tokens k_row_stride / v_row_stride elements apart (a
+ *          multiple of 8, at least Hkv * 256: slices of a fused projection are fine)
+ *   pos, mass : written for the new rows; either may be NULL
+ */
+hcadsa_status mla_cache_append(const hcadsa_bf16* K, const hcadsa_bf16* V, long long k_row_stride,
+                               long long v_row_stride, hcadsa_bf16* K_pool, hcadsa_bf16* V_pool,
+                               long long k_page_stride, long long v_page_stride, const int32_t* table,
+                               const int32_t* cu_q, const int32_t* kv_len, const int32_t* seen, int32_t* pos,
+                               float* mass, int B, int T, int n_pages, int page, int max_pages, int Hkv, int d,
+                               hcadsa_stream stream);
+
+/*
+ * Attention of the new tokens over the paged cache.  New token i of sequence b sees the rows
+ * s <= kv_len[b] - n_b + i (causal in row order, aligned to the end):
+ *     O[t,h] = sum_s softmax_s(scale <Q[t,h], K[s]>) V[s],   lse[t,h] = log sum_s exp(scale <Q[t,h], K[s]>)
+ * Query head h reads K/V head h / (Hq/Hkv).  A token that sees no row (kv_len[b] < n_b) gets O = 0,
+ * lse = -inf.  What lies in a page behind the last row of its sequence does not matter (NaN
+ * included).
+ *   Q   : [T, Hq, 256] bf16, tokens q_row_stride elements apart (a multiple of 8)
+ *   O   : [T, Hq, 256] bf16 (written for the tokens of the batch); lse: [T, Hq] fp32 or NULL
+ *   workspace : mla_paged_attn_fwd_workspace_size(...) bytes, 16-byte aligned, scratch: calls that
+ *               share it must be serialised.  The size depends on the current device's SM count.
+ * scale > 0 (HCADSA_ERR_SHAPE otherwise).  Results do not depend on timing.
+ */
+size_t mla_paged_attn_fwd_workspace_size(int B, int T, int Hq, int Hkv);
+hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,
+                                 const hcadsa_bf16* V_pool, long long k_page_stride, long long v_page_stride,
+                                 const int32_t* table, const int32_t* cu_q, const int32_t* kv_len, hcadsa_bf16* O,
+                                 float* lse, int B, int T, int n_pages, int page, int max_pages, int Hq, int Hkv,
+                                 int d, float scale, void* workspace, size_t workspace_bytes, hcadsa_stream stream);
+
+/*
+ * Attention weight per cached row: for every row s of sequence b's cache and K/V head,
+ *     mass[s] += sum over the new tokens t that see s and the heads h of the K/V head of
+ *                exp(scale <Q[t,h], K[s]> - lse[t,h])
+ * with the lse of mla_paged_attn_fwd on the same arguments.  ADDED to the pool rows' mass; rows of
+ * other sequences keep theirs.  Deterministic as long as no page belongs to two sequences of the
+ * batch (a shared row gets the sum of both, in either order).
+ *   lse : [T, Hq] fp32;  mass : [n_pages, page, Hkv] fp32 (accumulated)
+ *   workspace : as for the attention, mla_paged_attn_mass_workspace_size(...) bytes
+ */
+size_t mla_paged_attn_mass_workspace_size(int B, int T, int Hq, int Hkv);
+hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,
+                                  long long k_page_stride, const int32_t* table, const int32_t* cu_q,
+                                  const int32_t* kv_len, const float* lse, float* mass, int B, int T, int n_pages,
+                                  int page, int max_pages, int Hq, int Hkv, int d, float scale, void* workspace,
+                                  size_t workspace_bytes, hcadsa_stream stream);
+
+/*
+ * Which rows stay when every cache longer than `budget` rows is cut to it, per K/V head: the rows
+ * with pos < n_sink or pos >= seen[b] - n_recent, then those with the most mass, equal mass to the
+ * lower row, until `budget` rows stay (NaN counts as the most).  Rows that stay below row `budget`
+ * keep their place; entry i of
+ *   moves   : [B, Hkv, n_moves, 2] int32 (written): the i-th staying row >= budget and the i-th freed
+ *             row < budget, both ascending; entries past the last move are (-1, -1)
+ *   new_len : [B] int32 (written, not the kv_len array): min(kv_len, budget)
+ * A cache of at most `budget` rows gets no moves.  Nothing else is written: mla_cache_move makes
+ * the moves.  budget >= 1, 0 <= n_sink, 0 <= n_recent, n_sink + n_recent <= budget, n_moves at
+ * least min(budget, max_pages * page - budget) (HCADSA_ERR_SHAPE otherwise).
+ */
+hcadsa_status mla_evict_select(const float* mass, const int32_t* pos, const int32_t* table, const int32_t* kv_len,
+                               const int32_t* seen, int32_t* moves, int32_t* new_len, int B, int n_pages, int page,
+                               int max_pages, int Hkv, int budget, int n_sink, int n_recent, int n_moves,
+                               hcadsa_stream stream);
+
+/*
+ * Copies pool rows within their sequences: for every entry (from, to) of moves [B, Hkv, n_moves, 2],
+ * the K and V row (and pos and mass, unless NULL) of row `from` of sequence b and that K/V head go to
+ * row `to`.  Entries with a negative member are skipped.  No row may be written by two entries, or
+ * written by one and read by another (mla_evict_select's lists are of that kind: they read rows >=
+ * budget and write rows < budget).
+ */
+hcadsa_status mla_cache_move(const int32_t* moves, const int32_t* table, hcadsa_bf16* K_pool, hcadsa_bf16* V_pool,
+                             long long k_page_stride, long long v_page_stride, int32_t* pos, float* mass, int B,
+                             int n_moves, int n_pages, int page, int max_pages, int Hkv, int d,
+                             hcadsa_stream stream);
+
 /* ------------------------------------------------------------------ backward pass */
 
 /*

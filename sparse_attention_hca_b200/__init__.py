@@ -13,6 +13,11 @@ Functions (same names as the C ABI):
     csa_index_topk(q_idx, kc_idx, w_idx, k, blk, ...) -> idx (over compressed entries)
     dsa_sparse_attn_fwd(Q, K, V, idx, ...)            -> O  (or (O, lse))
     attn_gate_vha_fwd(O, cq, Wg, U, V)                -> Y (output gate + virtual-head mix)
+    mla_cache_append(K, V, K_pool, V_pool, ...)       -> rows of a chunk into a paged cache
+    mla_paged_attn_fwd(Q, K_pool, V_pool, ...)        -> O  (or (O, lse)) of a chunk over a paged cache
+    mla_paged_attn_mass(Q, K_pool, ..., lse)          -> mass (attention weight every cached row received)
+    mla_evict_select(mass, pos, ..., budget)          -> (moves, new_len)
+    mla_cache_move(moves, K_pool, V_pool, table)      -> makes the moves
     hcadsa_check_device_error()                       -> raises on a recorded device error
 """
 from __future__ import annotations
@@ -101,6 +106,21 @@ def lib() -> ctypes.CDLL:
             L.hca_attn_bwd.argtypes = [P, P, P, I, P, P, I, I, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P,
                                        S, P]
             L.hca_attn_bwd.restype = I
+            N = ctypes.c_longlong
+            L.mla_cache_append.argtypes = [P, P, N, N, P, P, N, N, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
+            L.mla_cache_append.restype = I
+            L.mla_paged_attn_fwd_workspace_size.argtypes = [I] * 4
+            L.mla_paged_attn_fwd_workspace_size.restype = S
+            L.mla_paged_attn_fwd.argtypes = [P, N, P, P, N, N, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, S, P]
+            L.mla_paged_attn_fwd.restype = I
+            L.mla_paged_attn_mass_workspace_size.argtypes = [I] * 4
+            L.mla_paged_attn_mass_workspace_size.restype = S
+            L.mla_paged_attn_mass.argtypes = [P, N, P, N, P, P, P, P, P, I, I, I, I, I, I, I, I, F, P, S, P]
+            L.mla_paged_attn_mass.restype = I
+            L.mla_evict_select.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, P]
+            L.mla_evict_select.restype = I
+            L.mla_cache_move.argtypes = [P, P, P, P, N, N, P, P, I, I, I, I, I, I, I, P]
+            L.mla_cache_move.restype = I
             _lib = L
     return _lib
 
@@ -514,3 +534,216 @@ def hca_attn_bwd(Q, Kc, Vc, Kw, Vw, O, dO, lse, *, win_start: int = 0, q_offset:
                         float(scale), _ptr(workspace), ws_bytes, _stream(stream))
     _check(st, "hca_attn_bwd")
     return dQ, (dKc if n_c else None), (dVc if n_c else None), dKw, dVw
+
+
+# ----------------------------------------------------------------------------- paged cache of the MLA layers
+
+
+def _need_pool(t, name, like=None):
+    """A pool [n_pages, page, Hkv, d] bf16: dense within a page, any page stride that keeps them apart."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 4 or (like is not None and t.shape != like.shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"{'[n_pages, page, Hkv, d]' if like is None else tuple(like.shape)}")
+    n_pages, page, Hkv, d = t.shape
+    st = t.stride()
+    if st[3] != 1 or (Hkv > 1 and st[2] != d) or (page > 1 and st[1] != Hkv * d) or (n_pages > 1 and
+                                                                                    st[0] < page * Hkv * d):
+        raise ValueError(f"{name} must be contiguous within a page, with pages apart (strides {st})")
+    return n_pages, page, Hkv, d, (st[0] if n_pages > 1 else page * Hkv * d)
+
+
+def _need_rows(t, name, H=None):
+    """Packed rows [T, H, d] bf16: dense within a row, any row stride that keeps them apart."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (H is not None and t.shape[1] != H):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, {'H' if H is None else H}, d]")
+    T, h, d = t.shape
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d) or (T > 1 and st[0] < h * d):
+        raise ValueError(f"{name} must be contiguous within a row, with rows apart (strides {st})")
+    return T, h, d, (st[0] if T > 1 else h * d)
+
+
+def _need_batch(table, kv_len, cu_q=None, seen=None):
+    _need(table, torch.int32, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
+    B, max_pages = table.shape
+    _need(kv_len, torch.int32, "kv_len", (B,))
+    if cu_q is not None:
+        _need(cu_q, torch.int32, "cu_q", (B + 1,))
+    if seen is not None:
+        _need(seen, torch.int32, "seen", (B,))
+    return B, max_pages
+
+
+def _alloc(stream, make):
+    """Device memory for a call on `stream`: taken from that stream's pool, so that the allocator
+    does not hand it out again before the call has run."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def mla_cache_append(K, V, K_pool, V_pool, table, cu_q, kv_len, *, seen=None, pos=None, mass=None, stream=None):
+    """K, V: [T, Hkv, 256] new rows, sequence b's at cu_q[b] .. cu_q[b+1]-1 -> rows kv_len[b] - n_b .. of its pages
+    in K_pool, V_pool [n_pages, page, Hkv, 256] (table [B, max_pages], cu_q [B + 1], kv_len [B] int32; kv_len counts
+    the new rows).  pos (int32) and mass (fp32) [n_pages, page, Hkv], where given: pos = seen - n_b + i (seen: [B]
+    int32, tokens so far; kv_len if None), mass = 0.  Returns (K_pool, V_pool)."""
+    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
+    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
+    T, _, dk, k_row = _need_rows(K, "K", Hkv)
+    Tv, _, dv, v_row = _need_rows(V, "V", Hkv)
+    if Tv != T or dk != d or dv != d:
+        raise ValueError(f"K and V have shapes {tuple(K.shape)} and {tuple(V.shape)}, expected [T, {Hkv}, {d}] of one T")
+    B, max_pages = _need_batch(table, kv_len, cu_q, seen)
+    if pos is not None:
+        _need(pos, torch.int32, "pos", (n_pages, page, Hkv))
+    if mass is not None:
+        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _on_device(K, V, K_pool, V_pool, table, cu_q, kv_len, seen, pos, mass)
+    st = lib().mla_cache_append(K.data_ptr(), V.data_ptr(), k_row, v_row, K_pool.data_ptr(), V_pool.data_ptr(),
+                                k_page, v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _addr(seen), _addr(pos), _addr(mass), B, T, n_pages, page,
+                                max_pages, Hkv, d, _stream(stream))
+    _check(st, "mla_cache_append")
+    return K_pool, V_pool
+
+
+def mla_paged_attn_fwd(Q, K_pool, V_pool, table, cu_q, kv_len, *, scale: float | None = None, O=None, lse=None,
+                       return_lse=False, workspace=None, stream=None):
+    """Q: [T, Hq, 256], sequence b's new tokens at cu_q[b] .. cu_q[b+1]-1 -> O [T, Hq, 256] (and lse [T, Hq] fp32) over
+    the kv_len[b] rows of its pages; new token i sees the rows <= kv_len[b] - n_b + i.  Pools, table and lengths as
+    for mla_cache_append.  Rows of O and lse behind cu_q[B] are left as they are."""
+    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
+    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
+    T, Hq, dq, q_row = _need_rows(Q, "Q")
+    if dq != d:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
+    B, max_pages = _need_batch(table, kv_len, cu_q)
+    if O is not None:
+        _need(O, torch.bfloat16, "O", (T, Hq, d))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (T, Hq))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device(Q, K_pool, V_pool, table, cu_q, kv_len, O, lse, workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dev = Q.device
+    if O is None:
+        O = _alloc(stream, lambda: torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev))
+    if return_lse and lse is None:
+        lse = _alloc(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
+    L = lib()
+    if workspace is None:
+        ws_bytes = L.mla_paged_attn_fwd_workspace_size(B, T, Hq, Hkv)
+        if ws_bytes:
+            workspace = _alloc(stream, lambda: torch.empty(ws_bytes, dtype=torch.uint8, device=dev))
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = L.mla_paged_attn_fwd(Q.data_ptr(), q_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), O.data_ptr(),
+                              _addr(lse), B, T, n_pages, page, max_pages, Hq, Hkv, d, scale, _addr(workspace),
+                              ws_bytes, _stream(stream))
+    _check(st, "mla_paged_attn_fwd")
+    return (O, lse) if return_lse else O
+
+
+def mla_paged_attn_mass(Q, K_pool, table, cu_q, kv_len, lse, *, scale: float | None = None, mass=None, workspace=None,
+                        stream=None):
+    """Attention weight that every cached row received from the new tokens: mass [n_pages, page, Hkv] fp32, added to
+    when given (zeros otherwise), += sum over the tokens that see the row and the heads of its K/V head of
+    exp(scale <q, k> - lse), with lse [T, Hq] fp32 from mla_paged_attn_fwd on the same arguments."""
+    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
+    T, Hq, dq, q_row = _need_rows(Q, "Q")
+    if dq != d:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
+    B, max_pages = _need_batch(table, kv_len, cu_q)
+    _need(lse, torch.float32, "lse", (T, Hq))
+    if mass is not None:
+        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device(Q, K_pool, table, cu_q, kv_len, lse, mass, workspace)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dev = Q.device
+    if mass is None:
+        mass = _alloc(stream, lambda: torch.zeros((n_pages, page, Hkv), dtype=torch.float32, device=dev))
+    L = lib()
+    if workspace is None:
+        ws_bytes = L.mla_paged_attn_mass_workspace_size(B, T, Hq, Hkv)
+        if ws_bytes:
+            workspace = _alloc(stream, lambda: torch.empty(ws_bytes, dtype=torch.uint8, device=dev))
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = L.mla_paged_attn_mass(Q.data_ptr(), q_row, K_pool.data_ptr(), k_page, table.data_ptr(),
+                               cu_q.data_ptr(), kv_len.data_ptr(), lse.data_ptr(), mass.data_ptr(), B, T, n_pages,
+                               page, max_pages, Hq, Hkv, d, scale, _addr(workspace), ws_bytes, _stream(stream))
+    _check(st, "mla_paged_attn_mass")
+    return mass
+
+
+def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int = 0, n_recent: int = 0, moves=None,
+                     new_len=None, stream=None):
+    """Cuts every cache longer than `budget` rows to it, per K/V head: rows with pos < n_sink or pos >= seen - n_recent
+    stay, then those with the most mass (ties to the lower row).  mass fp32, pos int32 [n_pages, page, Hkv]; kv_len, seen
+    [B] int32 (seen None: kv_len) -> moves [B, Hkv, n, 2] int32, entry i = (i-th staying row >= budget, i-th freed row <
+    budget), (-1, -1) past the last, n = min(budget, max_pages * page - budget); new_len [B] int32.  Writes nothing else:
+    mla_cache_move makes the moves."""
+    _need(mass, torch.float32, "mass")
+    if mass.dim() != 3:
+        raise ValueError(f"mass has shape {tuple(mass.shape)}, expected [n_pages, page, Hkv]")
+    n_pages, page, Hkv = mass.shape
+    _need(pos, torch.int32, "pos", mass.shape)
+    B, max_pages = _need_batch(table, kv_len, seen=seen)
+    n = max(0, min(budget, max_pages * page - budget))
+    if moves is not None:
+        _need(moves, torch.int32, "moves", (B, Hkv, n, 2))
+    if new_len is not None:
+        _need(new_len, torch.int32, "new_len", (B,))
+        if new_len.data_ptr() == kv_len.data_ptr():
+            raise ValueError("new_len must not be kv_len: kv_len is read while new_len is written")
+    _on_device(mass, pos, table, kv_len, seen, moves, new_len)
+    dev = mass.device
+    if moves is None:
+        moves = _alloc(stream, lambda: torch.empty((B, Hkv, n, 2), dtype=torch.int32, device=dev))
+    if new_len is None:
+        new_len = _alloc(stream, lambda: torch.empty(B, dtype=torch.int32, device=dev))
+    st = lib().mla_evict_select(mass.data_ptr(), pos.data_ptr(), table.data_ptr(), kv_len.data_ptr(), _addr(seen),
+                                moves.data_ptr(), new_len.data_ptr(), B, n_pages, page, max_pages, Hkv, budget, n_sink,
+                                n_recent, n, _stream(stream))
+    _check(st, "mla_evict_select")
+    return moves, new_len
+
+
+def mla_cache_move(moves, K_pool, V_pool, table, *, pos=None, mass=None, stream=None):
+    """Copies pool rows within their sequences: for every entry (from, to) >= 0 of moves [B, Hkv, n, 2] int32, row `from`
+    of sequence b and that K/V head (K, V, and pos and mass where given) goes to row `to`.  No row may be written twice,
+    or written by one entry and read by another.  Returns (K_pool, V_pool)."""
+    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
+    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
+    _need(table, torch.int32, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
+    B, max_pages = table.shape
+    _need(moves, torch.int32, "moves")
+    if moves.dim() != 4 or moves.shape[0] != B or moves.shape[1] != Hkv or moves.shape[3] != 2:
+        raise ValueError(f"moves has shape {tuple(moves.shape)}, expected [{B}, {Hkv}, n, 2]")
+    if pos is not None:
+        _need(pos, torch.int32, "pos", (n_pages, page, Hkv))
+    if mass is not None:
+        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _on_device(moves, table, K_pool, V_pool, pos, mass)
+    st = lib().mla_cache_move(moves.data_ptr(), table.data_ptr(), K_pool.data_ptr(), V_pool.data_ptr(),
+                              k_page, v_page, _addr(pos), _addr(mass), B, moves.shape[2], n_pages,
+                              page, max_pages, Hkv, d, _stream(stream))
+    _check(st, "mla_cache_move")
+    return K_pool, V_pool

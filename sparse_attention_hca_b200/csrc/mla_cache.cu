@@ -1,0 +1,204 @@
+// mla_cache.cu -- writes to the paged cache of the full-context (MLA) layers: a chunk's new rows
+// (mla_cache_append) and the moves that close the gaps an eviction left (mla_cache_move).
+//
+// Method: the mirrorspeed page, section "Hybrid sparse attention, 1/7 full context access": the
+// MLA layers keep every token's K and V.  A cache row is 256 bf16 per K/V head in each pool.
+//
+// Both kernels only copy 512-byte rows (one warp instruction: lane l moves bytes 16 l .. 16 l + 15),
+// so their bound is HBM: 2 KB of traffic per row pair and direction.
+#include "mla_host.h"
+
+namespace hcadsa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTokens = 8;  // new tokens of a block
+
+struct AppendParams {
+  PagedBatch s;
+  const uint16_t* K;
+  const uint16_t* V;
+  uint16_t* K_pool;
+  uint16_t* V_pool;
+  const int32_t* seen;
+  int32_t* pos;
+  float* mass;
+  long long k_row, v_row, k_page, v_page;  // strides in elements
+  int Hkv;
+};
+
+// A block owns kTokens packed tokens: all its threads look for the sequences that own them (one
+// pass over cu_q, no search chain), then a warp copies one (token, head) at a time.
+__global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p) {
+  __shared__ int owner[kTokens];
+  const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < kTokens) owner[threadIdx.x] = -1;
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.s.B; b += blockDim.x) {
+    const PagedSeq q = paged_seq(p.s, b, blockIdx.x == 0);
+    const int a = max(q.q0, t0), z = min(q.q0 + q.n, t0 + kTokens);
+    for (int t = a; t < z; ++t) owner[t - t0] = b;
+  }
+  __syncthreads();
+  const int n_tok = min(kTokens, p.s.T - t0);
+  const int page_mask = (1 << p.s.page_log2) - 1;
+  for (int u = warp; u < n_tok * p.Hkv; u += kWarps) {
+    const int i = u / p.Hkv, h = u - i * p.Hkv, t = t0 + i;
+    const int b = owner[i];
+    if (b < 0) continue;  // a packed row behind the last sequence
+    const uint4 k = reinterpret_cast<const uint4*>(p.K + (size_t)t * p.k_row + (size_t)h * kMlaD)[lane];
+    const uint4 v = reinterpret_cast<const uint4*>(p.V + (size_t)t * p.v_row + (size_t)h * kMlaD)[lane];
+    const PagedSeq q = paged_seq(p.s, b, false);
+    const int back = q.q0 + q.n - t;  // rows from this one to the end
+    const int r = q.len - back;
+    if (r < 0) {  // the cache is declared shorter than the chunk
+      if (lane == 0) raise_device_error(p.s.err, kErrDeviceBounds);
+      continue;
+    }
+    const int pg = paged_page(p.s, b, r);
+    if (pg < 0) continue;
+    const int in = r & page_mask;
+    const size_t row = (size_t)in * p.Hkv + h;
+    reinterpret_cast<uint4*>(p.K_pool + (size_t)pg * p.k_page + row * kMlaD)[lane] = k;
+    reinterpret_cast<uint4*>(p.V_pool + (size_t)pg * p.v_page + row * kMlaD)[lane] = v;
+    const size_t slot = (((size_t)pg << p.s.page_log2) * p.Hkv) + row;
+    if (lane == 0 && p.pos) p.pos[slot] = p.seen ? p.seen[b] - back : r;
+    if (lane == 1 && p.mass) p.mass[slot] = 0.0f;
+  }
+}
+
+struct MoveParams {
+  PagedBatch s;
+  const int2* moves;  // [B, Hkv, n_moves] (from, to)
+  uint16_t* K_pool;
+  uint16_t* V_pool;
+  int32_t* pos;
+  float* mass;
+  long long k_page, v_page;
+  int Hkv, n_moves, blocks_per_list;
+};
+
+constexpr int kMovesPerWarp = 8;
+
+// A warp takes 8 consecutive entries of one list: lane i < 8 reads entry i and looks both rows'
+// pages up, then all 16 row loads are in flight before the first store.
+__global__ void __launch_bounds__(32 * kWarps) move_kernel(const MoveParams p) {
+  const int list = blockIdx.x / p.blocks_per_list, part = blockIdx.x - list * p.blocks_per_list;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = (part * kWarps + warp) * kMovesPerWarp;
+  if (i0 >= p.n_moves) return;
+  const int b = list / p.Hkv, h = list - b * p.Hkv;
+  const int cap = p.s.max_pages << p.s.page_log2, page_mask = (1 << p.s.page_log2) - 1;
+  // pool row numbers (page << page_log2 | place) of this lane's entry; -1: nothing to move
+  long long from = -1, to = -1;
+  if (lane < kMovesPerWarp && i0 + lane < p.n_moves) {
+    const int2 m = p.moves[(size_t)list * p.n_moves + i0 + lane];
+    if (m.x >= 0 && m.y >= 0) {
+      if (m.x < cap && m.y < cap) {
+        const int pf = paged_page(p.s, b, m.x), pt = paged_page(p.s, b, m.y);
+        if (pf >= 0 && pt >= 0) {
+          from = ((long long)pf << p.s.page_log2) + (m.x & page_mask);
+          to = ((long long)pt << p.s.page_log2) + (m.y & page_mask);
+        }
+      } else {
+        raise_device_error(p.s.err, kErrDeviceBounds);
+      }
+    }
+  }
+  if (!__any_sync(0xffffffffu, from >= 0)) return;
+  if (from >= 0) {
+    const size_t sf = (size_t)from * p.Hkv + h, st = (size_t)to * p.Hkv + h;
+    if (p.pos) p.pos[st] = p.pos[sf];
+    if (p.mass) p.mass[st] = p.mass[sf];
+  }
+  uint4 k[kMovesPerWarp], v[kMovesPerWarp];
+#pragma unroll
+  for (int i = 0; i < kMovesPerWarp; ++i) {
+    const long long f = __shfl_sync(0xffffffffu, from, i);
+    if (f < 0) continue;
+    const size_t pg = (size_t)(f >> p.s.page_log2), row = (size_t)((int)f & page_mask) * p.Hkv + h;
+    k[i] = reinterpret_cast<const uint4*>(p.K_pool + pg * p.k_page + row * kMlaD)[lane];
+    v[i] = reinterpret_cast<const uint4*>(p.V_pool + pg * p.v_page + row * kMlaD)[lane];
+  }
+#pragma unroll
+  for (int i = 0; i < kMovesPerWarp; ++i) {
+    const long long f = __shfl_sync(0xffffffffu, from, i), t = __shfl_sync(0xffffffffu, to, i);
+    if (f < 0) continue;
+    const size_t pg = (size_t)(t >> p.s.page_log2), row = (size_t)((int)t & page_mask) * p.Hkv + h;
+    reinterpret_cast<uint4*>(p.K_pool + pg * p.k_page + row * kMlaD)[lane] = k[i];
+    reinterpret_cast<uint4*>(p.V_pool + pg * p.v_page + row * kMlaD)[lane] = v[i];
+  }
+}
+
+}  // namespace
+}  // namespace hcadsa
+
+extern "C" hcadsa_status mla_cache_append(const hcadsa_bf16* K, const hcadsa_bf16* V, long long k_row_stride,
+                                          long long v_row_stride, hcadsa_bf16* K_pool, hcadsa_bf16* V_pool,
+                                          long long k_page_stride, long long v_page_stride, const int32_t* table,
+                                          const int32_t* cu_q, const int32_t* kv_len, const int32_t* seen,
+                                          int32_t* pos, float* mass, int B, int T, int n_pages, int page,
+                                          int max_pages, int Hkv, int d, hcadsa_stream stream) {
+  using namespace hcadsa;
+  if (T < 0) return HCADSA_ERR_SHAPE;
+  if (B > 0 && T > 0 && (!K || !V || !K_pool || !V_pool || !table || !cu_q || !kv_len)) return HCADSA_ERR_NULL;
+  HCADSA_TRY(check_paged_sizes(B, n_pages, page, max_pages, Hkv));
+  if (d != kMlaD) return HCADSA_ERR_UNSUPPORTED;
+  HCADSA_TRY(check_row_stride(k_row_stride, Hkv));
+  HCADSA_TRY(check_row_stride(v_row_stride, Hkv));
+  HCADSA_TRY(check_page_stride(k_page_stride, page, Hkv));
+  HCADSA_TRY(check_page_stride(v_page_stride, page, Hkv));
+  if (!aligned16(K) || !aligned16(V) || !aligned16(K_pool) || !aligned16(V_pool) || !aligned4(table) ||
+      !aligned4(cu_q) || !aligned4(kv_len) || !aligned4(seen) || !aligned4(pos) || !aligned4(mass))
+    return HCADSA_ERR_ALIGN;
+  if (B == 0 || T == 0) return HCADSA_OK;
+  AppendParams p;
+  p.s = paged_batch(table, cu_q, kv_len, B, T, n_pages, page, max_pages);
+  p.K = K;
+  p.V = V;
+  p.K_pool = K_pool;
+  p.V_pool = V_pool;
+  p.seen = seen;
+  p.pos = pos;
+  p.mass = mass;
+  p.k_row = k_row_stride;
+  p.v_row = v_row_stride;
+  p.k_page = k_page_stride;
+  p.v_page = v_page_stride;
+  p.Hkv = Hkv;
+  append_kernel<<<(T + kTokens - 1) / kTokens, 32 * kWarps, 0, as_stream(stream)>>>(p);
+  return launch_status();
+}
+
+extern "C" hcadsa_status mla_cache_move(const int32_t* moves, const int32_t* table, hcadsa_bf16* K_pool,
+                                        hcadsa_bf16* V_pool, long long k_page_stride, long long v_page_stride,
+                                        int32_t* pos, float* mass, int B, int n_moves, int n_pages, int page,
+                                        int max_pages, int Hkv, int d, hcadsa_stream stream) {
+  using namespace hcadsa;
+  if (n_moves < 0) return HCADSA_ERR_SHAPE;
+  if (B > 0 && n_moves > 0 && (!moves || !table || !K_pool || !V_pool)) return HCADSA_ERR_NULL;
+  HCADSA_TRY(check_paged_sizes(B, n_pages, page, max_pages, Hkv));
+  if (d != kMlaD) return HCADSA_ERR_UNSUPPORTED;
+  HCADSA_TRY(check_page_stride(k_page_stride, page, Hkv));
+  HCADSA_TRY(check_page_stride(v_page_stride, page, Hkv));
+  if (!aligned16(K_pool) || !aligned16(V_pool) || (reinterpret_cast<uintptr_t>(moves) & 7u) || !aligned4(table) ||
+      !aligned4(pos) || !aligned4(mass))
+    return HCADSA_ERR_ALIGN;
+  if (B == 0 || n_moves == 0) return HCADSA_OK;
+  MoveParams p;
+  p.s = paged_batch(table, nullptr, nullptr, B, 0, n_pages, page, max_pages);
+  p.moves = reinterpret_cast<const int2*>(moves);
+  p.K_pool = K_pool;
+  p.V_pool = V_pool;
+  p.pos = pos;
+  p.mass = mass;
+  p.k_page = k_page_stride;
+  p.v_page = v_page_stride;
+  p.Hkv = Hkv;
+  p.n_moves = n_moves;
+  p.blocks_per_list = (n_moves - 1) / (kWarps * kMovesPerWarp) + 1;
+  const long long blocks = (long long)B * Hkv * p.blocks_per_list;
+  if (blocks > 2147483647LL) return HCADSA_ERR_UNSUPPORTED;
+  move_kernel<<<(unsigned)blocks, 32 * kWarps, 0, as_stream(stream)>>>(p);
+  return launch_status();
+}
