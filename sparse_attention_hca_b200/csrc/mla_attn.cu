@@ -1,100 +1,686 @@
 // mla_attn.cu -- attention of a chunk of new tokens over the paged cache of the full-context
-// (MLA) layers (mla_paged_attn_fwd).
+// (MLA) layers on sm_100a (mla_paged_attn_fwd): TMA page loads, tcgen05 MMA on CTA pairs, TMEM.
 //
 // Method: the mirrorspeed page, section "Hybrid sparse attention, 1/7 full context access": the
 // MLA layers see every token; heads are 256 wide.  New token i of a sequence sees the rows
 // <= base + i of its cache (base: rows before the chunk):
 //     O = sum_s p_s v_s,  p = softmax_s(scale <q, k_s>),  lse = log sum_s exp(scale <q, k_s>)
 //
-// One warp per (token, query head), lane l holding channels 8 l .. 8 l + 7: one pass over the
-// visible rows with a running maximum and sum.
+// Tiles: the g query heads of a K/V head share its rows, so a row tile is 256 (token, head) rows
+// = 256 / g tokens; a key tile is 128 cache rows.  A CTA pair computes a row tile against a run of
+// key tiles: CTA r holds rows 128 r .. 128 r + 127 (its TMEM lanes), and loads half of every K and
+// V tile -- K rows 64 r .. +63, V columns 128 r .. +127 -- which the pair's MMAs (cta_group::2,
+// M = 256) read from both.  One CTA alone (M = 128) would need 64 bytes of K and V per SM cycle at
+// the full MMA rate, the limit of the L2; the pair needs 32.
+//   S  = Q (A, smem) * K^T (B, smem, K-major)        128 columns of TMEM, two buffers
+//   O += P (A, TMEM, bf16 over its own S) * V (B, smem, MN-major)   256 columns of TMEM
+// S and O together are all 512 columns.  Roles per CTA: warp 0 TMA (both CTAs; the lanes issue a
+// tile's page boxes side by side), warp 1 the MMA thread (leader CTA), warps 4-7 softmax, one
+// thread per row: the whole row of a tile is in registers, so its maximum and sum need no
+// exchange.  The reference maximum moves only when it is exceeded by 2^8 (lazy rescale of O).
+//
+// Schedule: the (row tile, key tile) products of the whole batch form one list -- sequence, K/V
+// head, row tile, key tile -- whose length follows in closed form from the lengths.  Pair c of G
+// takes the products [c N / G, (c+1) N / G): equal work for prompts, chunks and single tokens alike,
+// decided on the device (the host never sees the lengths).  A row tile that several pairs share
+// leaves unnormalised fp32 rows and (max, sum) in the workspace -- at most two such pieces per
+// pair -- and combine_kernel merges them in list order: the result does not depend on timing.
+//
+// Rows behind the end of a sequence in its last page may hold anything.  Their scores are replaced
+// before the softmax, and since 0 * NaN is NaN, the V rows of such a tile are cleared in shared
+// memory by the softmax warps before the PV product: that tile's V completes on a barrier of its
+// own CTA (v_tail) instead of the leader's.
+#include <mutex>
+
 #include "mla_host.h"
+#include "pair.cuh"
 
 namespace hcadsa {
 namespace {
 
+constexpr int kKeyTile = 128;
+constexpr int kRows = 256;                 // (token, head) rows of a row tile
+constexpr int kSlots = 5;                  // ring of K and V half tiles
+constexpr int kSlotBytes = 32 * 1024;      // K: 64 rows x 256, or V: 128 rows x 128
+constexpr int kQBytes = 64 * 1024;         // 128 rows x 256
+constexpr int kQChunk = 16 * 1024, kKChunk = 8 * 1024, kVChunk = 16 * 1024;  // 64 columns of each
+constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemS = 256;           // S buffers at columns 256 and 384; O at 0
+constexpr float kLazyRescale = 8.0f;
+constexpr int kMetaInts = 8;
+
 struct Params {
   PagedBatch s;
-  const uint16_t* Q;
-  const uint16_t* K_pool;
-  const uint16_t* V_pool;
   uint16_t* O;
   float* lse;
-  long long q_row, k_page, v_page;
-  int Hq, Hkv;
-  float scale;
+  float* ws_O;   // [2 G][256][256]: pair c's piece that began before its range (2 c) and after (2 c + 1)
+  float* ws_ml;  // [2 G][2][256]: reference maximum (log2 units), sum
+  int* ws_meta;  // [G][kMetaInts]
+  int Hq, Hkv, g_log2, box_log2;
+  float scale_log2;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct __align__(8) Barriers {
+  uint64_t q_full, q_empty;
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t s_full[2], p_ready[2];
+  uint64_t pv_done;
+  uint64_t v_tail[2];  // alternating: a piece's tail may land while the piece before waits for its own
+};
+
+// ------------------------------------------------------------------ the list of products
+
+// One sequence's part of the list (of one K/V head).
+struct SeqTiles {
+  int base, n, len, tq_log2;
+  __host__ __device__ int row_tiles() const { return (n + (1 << tq_log2) - 1) >> tq_log2; }
+  // key tiles of row tile i: up to the last row its last token sees.  A sequence declared shorter
+  // than its chunk (base < 0) has rows that see nothing; its row tiles take every key tile, at
+  // least one, and the mask does the rest.
+  __host__ __device__ int key_tiles(int i) const {
+    if (base < 0) return len > 0 ? (len + kKeyTile - 1) / kKeyTile : 1;
+    const long long last = (long long)(i + 1) << tq_log2;
+    return (int)((base + (last < n ? last : n) + kKeyTile - 1) / kKeyTile);
   }
+  // key tiles of the row tiles before i, in closed form: sum over k = 1 .. i of
+  // ceil((base + k tq) / 128), whose terms grow by one every 128 / tq row tiles
+  __host__ __device__ long long before(int i) const {
+    if (base < 0) return (long long)i * key_tiles(0);
+    const int rem = base % kKeyTile;
+    long long sum = (long long)i * (base / kKeyTile);
+    if (tq_log2 >= 8) {
+      sum += (long long)i * (i + 1) + (rem > 0 ? i : 0);
+    } else {
+      const int p_log2 = 7 - tq_log2, p = 1 << p_log2;
+      const long long a = i >> p_log2, r = i & (p - 1);
+      const int ones = (kKeyTile - rem) >> tq_log2;  // terms of the first 128 / tq that are 1, not 2
+      const auto part = [&](long long x) { return x + (x > ones ? x - ones : 0); };
+      sum += a * part(p) + p * (a * (a - 1) / 2) + a * r + part(r);
+    }
+    if (i > 0 && i == row_tiles()) {  // the last row tile ends with the cache
+      const long long full = base + ((long long)i << tq_log2);
+      sum -= (full + kKeyTile - 1) / kKeyTile - key_tiles(i - 1);
+    }
+    return sum;
+  }
+  // the row tile that holds product w of the list
+  __host__ __device__ int find(long long w) const {
+    int lo = 0, hi = row_tiles();
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) <= w) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2) {
+  SeqTiles t;
+  t.base = q.base;
+  t.n = q.n;
+  t.len = q.len;
+  t.tq_log2 = tq_log2;
+  return t;
 }
 
-__global__ void __launch_bounds__(256) attn_kernel(const Params p) {
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ int owner;
-  if (threadIdx.x == 0) owner = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.s.B; b += blockDim.x) {
-    const PagedSeq q = paged_seq(p.s, b, t == 0);
-    if (t >= q.q0 && t < q.q0 + q.n) owner = b;
-  }
-  __syncthreads();
-  const int b = owner;
-  if (b < 0) return;
-  const PagedSeq q = paged_seq(p.s, b, false);
-  const int n_vis = min(q.len, q.base + (t - q.q0) + 1);
-  const int page_mask = (1 << p.s.page_log2) - 1;
-  for (int h = blockIdx.y * 8 + warp; h < p.Hq; h += 8 * gridDim.y) {
-    const int hk = h / (p.Hq / p.Hkv);
-    float qf[8], o[8] = {};
-    unpack8(reinterpret_cast<const uint4*>(p.Q + (size_t)t * p.q_row + (size_t)h * kMlaD)[lane], qf);
-    float m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < n_vis; ++i) {
-      const int pg = paged_page(p.s, b, i);
-      float kf[8] = {}, vf[8] = {};
-      if (pg >= 0) {
-        const size_t row = ((size_t)(i & page_mask) * p.Hkv + hk) * kMlaD;
-        unpack8(reinterpret_cast<const uint4*>(p.K_pool + (size_t)pg * p.k_page + row)[lane], kf);
-        unpack8(reinterpret_cast<const uint4*>(p.V_pool + (size_t)pg * p.v_page + row)[lane], vf);
-      }
-      float x = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) x = fmaf(qf[c], kf[c], x);
-#pragma unroll
-      for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-      x *= p.scale;
-      const float mn = fmaxf(m, x), a = expf(m - mn), w = expf(x - mn);
-      m = mn;
-      l = fmaf(l, a, w);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) o[c] = fmaf(o[c], a, w * vf[c]);
+struct Start {
+  long long count;  // products of this pair
+  int b, h, i, j;   // where they begin
+};
+
+// Walks a pair's pieces: runs of key tiles of one row tile.
+struct Walk {
+  const Params& p;
+  long long left;
+  int b, h, i, j0, j1, n_keys, tq_log2;
+  PagedSeq q;
+  SeqTiles t;
+  __device__ Walk(const Params& p_, const Start& s) : p(p_) {
+    tq_log2 = 8 - p.g_log2;
+    left = s.count;
+    b = s.b;
+    h = s.h;
+    i = s.i;
+    j0 = s.j;
+    if (left > 0) {
+      load();
+      cut();
     }
-    const float inv = n_vis > 0 ? 1.0f / l : 0.0f;
-    const size_t row = (size_t)t * p.Hq + h;
-    uint4 w;
-    w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-    w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-    w.z = pack_bf16x2(o[4] * inv, o[5] * inv);
-    w.w = pack_bf16x2(o[6] * inv, o[7] * inv);
-    reinterpret_cast<uint4*>(p.O + row * kMlaD)[lane] = w;
-    if (p.lse && lane == 0) p.lse[row] = n_vis > 0 ? m + logf(l) : -INFINITY;
   }
+  __device__ bool done() const { return left <= 0; }
+  __device__ int tiles() const { return j1 - j0; }
+  __device__ int first_token() const { return i << tq_log2; }
+  __device__ void next() {
+    left -= j1 - j0;
+    if (left <= 0) return;
+    j0 = 0;
+    if (++i == t.row_tiles()) {
+      i = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.s.B) {  // cannot happen unless the lengths change under the kernel
+            left = 0;
+            return;
+          }
+          load();
+        } while (t.n == 0);
+      }
+    }
+    cut();
+  }
+
+ private:
+  __device__ void load() {
+    q = paged_seq(p.s, b, false);
+    t = seq_tiles(q, tq_log2);
+  }
+  __device__ void cut() {
+    n_keys = t.key_tiles(i);
+    const long long e = (long long)j0 + left;
+    j1 = e < n_keys ? (int)e : n_keys;
+  }
+};
+
+// Every thread of the CTA: this pair's share of the list.
+__device__ __forceinline__ void find_start(const Params& p, int pair, int n_pairs, Start* out) {
+  __shared__ long long sums[kThreads / 32 + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tq_log2 = 8 - p.g_log2;
+  auto work_of = [&](int b, bool report) -> long long {
+    if (b >= p.s.B) return 0;
+    const SeqTiles t = seq_tiles(paged_seq(p.s, b, report), tq_log2);
+    return t.n > 0 ? t.before(t.row_tiles()) * p.Hkv : 0;
+  };
+  // inclusive prefix over the CTA's threads, and its total
+  auto scan = [&](long long x, long long& total) -> long long {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    __syncthreads();
+    return before + x;
+  };
+  long long mine = 0, all;
+  for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
+  scan(mine, all);
+  // a short list goes to as many pairs as it has products, so that consecutive pieces of a row
+  // tile always lie in consecutive pairs
+  const int n = all < n_pairs ? (int)all : n_pairs;
+  const long long lo = pair < n ? all * pair / n : 0, hi = pair < n ? all * (pair + 1) / n : 0;
+  if (tid == 0) out->count = hi - lo;
+  long long done = 0;
+  for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
+    const long long w = work_of(b0 + tid, false);
+    long long total;
+    const long long upto = done + scan(w, total), from = upto - w;
+    if (from <= lo && lo < upto) {
+      const SeqTiles t = seq_tiles(paged_seq(p.s, b0 + tid, false), tq_log2);
+      const long long per_head = w / p.Hkv, r = lo - from;
+      out->b = b0 + tid;
+      out->h = (int)(r / per_head);
+      const long long in = r - out->h * per_head;
+      out->i = t.find(in);
+      out->j = (int)(in - t.before(out->i));
+    }
+    done += total;
+    if (done > lo) break;
+  }
+  __syncthreads();
 }
+
+// ------------------------------------------------------------------ the kernel
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + kQBytes;
+  __shared__ Barriers bar;
+  __shared__ Start start;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();  // 0: the leader, which issues the MMAs
+  const int pair = (int)blockIdx.x >> 1, n_pairs = (int)gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.q_empty, 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bar.full[s], 1);
+      mbar_init(&bar.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.p_ready[s], 8);  // the softmax warps of both CTAs
+    }
+    mbar_init(&bar.pv_done, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&bar.v_tail[s], 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&tmem_base_sh, 512);
+  find_start(p, pair, n_pairs, &start);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  const int box_rows = 1 << p.box_log2;
+  // whether key tile j holds rows behind the sequence's end that a page box brings in
+  auto is_tail = [&](int len, int j) { return (len & (box_rows - 1)) != 0 && len / kKeyTile == j; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (all lanes)
+    const int n_tma = 256 >> p.box_log2;  // boxes of a half tile: K 64 / box rows x 4 chunks, V 128 / box rows x 2
+    const int kbox = lane >> 2, kchunk = lane & 3, vbox = lane >> 1, vchunk = lane & 1;
+    const int page_mask = (1 << p.s.page_log2) - 1;
+    uint32_t u = 0;  // half tiles issued: slot u % kSlots
+    uint32_t it = 0, tails = 0;
+    bool ok = true;
+    for (Walk w(p, start); !w.done() && ok; w.next(), ++it) {
+      const int J = w.tiles();
+      auto page_of = [&](int row) -> int {  // a page that is not there: zeros (outside the tensor map)
+        if (lane >= n_tma || row >= w.q.len) return p.s.n_pages;
+        const int pg = paged_page(p.s, w.b, row);
+        return pg < 0 ? p.s.n_pages : pg;
+      };
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (it & 1) ^ 1, &abort_flag, p.s.err));
+      if (!ok) break;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(&bar.q_full, 2 * kQBytes);
+        const uint32_t full = cluster_addr(&bar.q_full, 0);
+        const int tok = w.q.q0 + w.first_token() + (int)(rank << (7 - p.g_log2));
+        for (int c = 0; c < 4; ++c)
+          tma_load_3d_pair(sQ + c * kQChunk, &map_q, full, c * 64, w.h << p.g_log2, tok);
+      }
+      __syncwarp();
+      int pk = page_of(w.j0 * kKeyTile + 64 * (int)rank + (kbox << p.box_log2)), pv = 0;
+      for (int step = 0; step <= J && ok; ++step) {
+        const int j = w.j0 + step;
+        // the pages of the next K tile and of this step's V tile of the next step are looked up ahead
+        int pk_next = 0, pv_next = 0;
+        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + 64 * (int)rank + (kbox << p.box_log2));
+        if (step < J) pv_next = page_of(j * kKeyTile + (vbox << p.box_log2));
+        if (step < J) {
+          const uint32_t s = u % kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], ((u / kSlots) & 1) ^ 1, &abort_flag, p.s.err));
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kSlotBytes);
+          __syncwarp();
+          if (lane < n_tma) {
+            const int row = j * kKeyTile + 64 * (int)rank + (kbox << p.box_log2);
+            tma_load_4d_pair(sRing + s * kSlotBytes + kchunk * kKChunk + (kbox << p.box_log2) * 128, &map_k,
+                             cluster_addr(&bar.full[s], 0), kchunk * 64, w.h, row & page_mask, pk);
+          }
+          ++u;
+        }
+        if (step >= 1) {
+          const uint32_t s = u % kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], ((u / kSlots) & 1) ^ 1, &abort_flag, p.s.err));
+          if (!ok) break;
+          const int row = (j - 1) * kKeyTile + (vbox << p.box_log2);
+          uint8_t* dst = sRing + s * kSlotBytes + vchunk * kVChunk + (vbox << p.box_log2) * 128;
+          const int col = 128 * (int)rank + vchunk * 64;
+          if (is_tail(w.q.len, j - 1)) {
+            uint64_t* tail = &bar.v_tail[tails++ & 1];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(tail, kSlotBytes);
+              if (rank == 0) mbar_arrive(&bar.full[s]);
+            }
+            __syncwarp();
+            if (lane < n_tma) tma_load_4d(dst, &map_v, tail, col, w.h, row & page_mask, pv);
+          } else {
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kSlotBytes);
+            __syncwarp();
+            if (lane < n_tma)
+              tma_load_4d_pair(dst, &map_v, cluster_addr(&bar.full[s], 0), col, w.h, row & page_mask, pv);
+          }
+          ++u;
+        }
+        pk = pk_next;
+        pv = pv_next;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeyTile, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(kRows, kMlaD, false, true);
+      const uint32_t sQa = smem_u32(sQ), sRa = smem_u32(sRing);
+      const uint64_t dq = smem_desc_sw128(sQa, 16, 1024);
+      uint32_t u = 0, it = 0, g = 0;  // g: key tiles so far (S buffer and barrier phases)
+      bool ok = true;
+      for (Walk w(p, start); !w.done() && ok; w.next(), ++it) {
+        const int J = w.tiles();
+        ok = mbar_wait(&bar.q_full, it & 1, &abort_flag, p.s.err);
+        for (int step = 0; step <= J && ok; ++step) {
+          if (step < J) {
+            const uint32_t gs = g + step, s = u % kSlots;
+            ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, 1024);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
+                mma_ss_pair(tmem + kTmemS + (gs & 1) * kKeyTile, dq + (uint64_t)((c * kQChunk + kk * 32) >> 4),
+                            dk + (uint64_t)((c * kKChunk + kk * 32) >> 4), idesc_s, (c | kk) != 0);
+            mma_commit_pair(&bar.empty[s]);
+            mma_commit_pair(&bar.s_full[gs & 1]);
+            if (step == J - 1) mma_commit_pair(&bar.q_empty);
+            ++u;
+          }
+          if (step >= 1) {
+            const uint32_t gj = g + step - 1, s = u % kSlots;
+            ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err) &&
+                 mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tP = tmem + kTmemS + (gj & 1) * kKeyTile;  // bf16 pairs: 64 columns
+            const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, kVChunk, 1024);
+#pragma unroll
+            for (int kk = 0; kk < kKeyTile / 16; ++kk)
+              mma_ts_pair(tmem, tP + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (step > 1 || kk > 0) ? 1u : 0u);
+            mma_commit_pair(&bar.empty[s]);
+            mma_commit_pair(&bar.pv_done);
+            ++u;
+          }
+        }
+        g += J;
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax and output (one thread per row)
+    const int quarter = warp & 3;
+    const int row = (int)rank * 128 + quarter * 32 + lane;  // row of the row tile
+    const int my_tok = row >> p.g_log2, my_head = row & ((1 << p.g_log2) - 1);
+    const uint32_t t_lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int tid = quarter * 32 + lane;
+    uint32_t g = 0, u = 0, tails = 0;
+    bool ok = true;
+    int head_flag = 0, tail_flag = 0, tail_tok = 0, tail_n = 0, tail_h = 0;  // for ws_meta
+    for (Walk w(p, start); !w.done(); w.next()) {
+      const int J = w.tiles();
+      const int tok = w.first_token() + my_tok;  // token of the sequence
+      const bool valid = tok < w.q.n;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      const int n_vis = min(w.q.base + tok + 1, w.q.len);  // rows this row sees (may be <= 0)
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int jj = 0; jj < J; ++jj, ++g) {
+        const int j = w.j0 + jj;
+        ok = mbar_wait(&bar.s_full[g & 1], (g >> 1) & 1, &abort_flag, p.s.err) && ok;
+        tc_fence_after();
+        if (warp_valid) {
+          const uint32_t tS = t_lanes + kTmemS + (g & 1) * kKeyTile;
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + c * 32, s[c]);
+          tmem_wait_ld_regs2(s[0], s[1]);
+          tmem_wait_ld_regs2(s[2], s[3]);
+          const int vis = n_vis - j * kKeyTile;
+          if (!__all_sync(0xffffffffu, vis >= kKeyTile)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (c * 32 + x >= vis) s[c][x] = 0xff800000u;
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(s[c][x]));
+          const float xt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          bool resc = false;
+          float alpha = 1.0f;
+          if (m_run == -INFINITY) {
+            m_run = xt;  // nothing visible so far: O is all zeros, or not yet written
+          } else if (xt > m_run + kLazyRescale) {
+            alpha = fast_exp2(m_run - xt);
+            m_run = xt;
+            resc = true;
+          }
+          const float m_ref = m_run == -INFINITY ? 0.0f : m_run;
+          l_run *= alpha;
+          float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pw[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float p0 = fast_exp2(fmaf(__uint_as_float(s[c][2 * x]), p.scale_log2, -m_ref));
+              const float p1 = fast_exp2(fmaf(__uint_as_float(s[c][2 * x + 1]), p.scale_log2, -m_ref));
+              l4[(2 * x) & 3] += p0;
+              l4[(2 * x + 1) & 3] += p1;
+              pw[x] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tS + c * 16, pw);
+          }
+          l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          if (__any_sync(0xffffffffu, resc)) {
+            // O holds every PV of this piece up to the previous tile; this tile's waits for p_ready
+            ok = mbar_wait(&bar.pv_done, (g - 1) & 1, &abort_flag, p.s.err) && ok;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[32];
+              tmem_ld32_nowait(t_lanes + c * 32, o);
+              tmem_wait_ld_regs(o);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tmem_st32(t_lanes + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        if (is_tail(w.q.len, j)) {
+          // V of the piece's last tile: clear the rows behind the sequence's end, up to the box's end
+          ok = mbar_wait(&bar.v_tail[tails & 1], (tails >> 1) & 1, &abort_flag, p.s.err) && ok;
+          ++tails;
+          const int r0 = w.q.len & (kKeyTile - 1), r1 = (r0 + box_rows - 1) & ~(box_rows - 1);
+          uint8_t* slot = sRing + ((u + 2 * J - 1) % kSlots) * kSlotBytes;
+          for (int e = tid; e < (r1 - r0) * 16; e += 128) {
+            const int r = r0 + (e >> 4), x = e & 15;
+            *reinterpret_cast<uint4*>(slot + (x >> 3) * kVChunk + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(&bar.p_ready[g & 1], 0));
+      }
+      u += 2 * J;
+      // ---- output of the piece, once its last PV is done.  The last tile's scores only showed that
+      // the PV two tiles before it was: the one in between is waited for first, or its parity would
+      // be taken for the last one's.
+      if (g >= 2) ok = mbar_wait(&bar.pv_done, g & 1, &abort_flag, p.s.err) && ok;
+      ok = mbar_wait(&bar.pv_done, (g - 1) & 1, &abort_flag, p.s.err) && ok;
+      tc_fence_after();
+      const bool whole = w.j0 == 0 && w.j1 == w.n_keys;
+      if (warp_valid) {
+        const size_t orow = (size_t)(w.q.q0 + tok) * p.Hq + (w.h << p.g_log2) + my_head;
+        const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+        const int slot = 2 * pair + (w.j0 == 0 ? 1 : 0);
+        if (valid) {
+          if (whole) {
+            if (p.lse) p.lse[orow] = l_run > 0.0f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+          } else {
+            p.ws_ml[(size_t)slot * 2 * kRows + row] = m_run;
+            p.ws_ml[(size_t)slot * 2 * kRows + kRows + row] = l_run;
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32_nowait(t_lanes + c * 32, o);
+          tmem_wait_ld_regs(o);
+          if (valid && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.O + orow * kMlaD + c * 32);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 v;
+              v.x = pack_bf16x2(__uint_as_float(o[8 * x + 0]) * inv, __uint_as_float(o[8 * x + 1]) * inv);
+              v.y = pack_bf16x2(__uint_as_float(o[8 * x + 2]) * inv, __uint_as_float(o[8 * x + 3]) * inv);
+              v.z = pack_bf16x2(__uint_as_float(o[8 * x + 4]) * inv, __uint_as_float(o[8 * x + 5]) * inv);
+              v.w = pack_bf16x2(__uint_as_float(o[8 * x + 6]) * inv, __uint_as_float(o[8 * x + 7]) * inv);
+              dst[x] = v;
+            }
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * kRows + row) * kMlaD + c * 32);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!whole) {
+        if (w.j0 > 0) {
+          head_flag = w.j1 == w.n_keys ? 2 : 1;
+        } else {
+          tail_flag = 1;
+          tail_tok = w.q.q0 + w.first_token();
+          tail_n = min(1 << w.tq_log2, w.q.n - w.first_token());
+          tail_h = w.h;
+        }
+      }
+    }
+    if (rank == 0 && tid == 0) {
+      int* m = p.ws_meta + pair * kMetaInts;
+      m[0] = head_flag;
+      m[1] = tail_flag;
+      m[2] = tail_tok;
+      m[3] = tail_n;
+      m[4] = tail_h;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Merges the pieces of a row tile that began in pair c's range and went on in pairs c+1, c+2, ...
+// (piece k >= 1 is the one pair c + k began with), in that order: with M the largest of the maxima,
+//     O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
+// One warp per row; the lanes read the pieces' (max, sum) side by side, so the loads of the rows
+// themselves (lane l: columns 8 l .. 8 l + 7) do not wait on one another.
+constexpr int kCombineWarps = 8;
+constexpr int kMaxPairs = 128;
+
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p, int n_pairs) {
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  const int* meta = p.ws_meta + c * kMetaInts;
+  if (!meta[1]) return;
+  const int tok = row >> p.g_log2;
+  if (tok >= meta[3]) return;
+  int n = 1;  // pieces
+  for (int k0 = c + 1; k0 < n_pairs; k0 += 32) {
+    const int flag = k0 + lane < n_pairs ? p.ws_meta[(k0 + lane) * kMetaInts] : 2;
+    const uint32_t last = __ballot_sync(0xffffffffu, flag != 1);
+    if (last) {
+      n += __ffs(last);
+      break;
+    }
+    n += 32;
+  }
+  n = min(n, n_pairs - c);
+  float m[kMaxPairs / 32], l[kMaxPairs / 32], M = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kMaxPairs / 32; ++q) {
+    const int k = q * 32 + lane;
+    m[q] = -INFINITY;
+    l[q] = 0.0f;
+    if (k < n) {
+      const float* ml = p.ws_ml + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 * kRows + row;
+      m[q] = ml[0];
+      l[q] = ml[kRows];
+    }
+    if (l[q] > 0.0f) M = fmaxf(M, m[q]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float den = 0.0f, acc[8] = {};
+#pragma unroll
+  for (int q = 0; q < kMaxPairs / 32; ++q) {
+    const float w_mine = l[q] > 0.0f ? exp2f(m[q] - M) : 0.0f;
+    const int n_q = min(32, n - q * 32);
+#pragma unroll 4
+    for (int k = 0; k < n_q; ++k) {
+      const float w = __shfl_sync(0xffffffffu, w_mine, k), lk = __shfl_sync(0xffffffffu, l[q], k);
+      const int piece = q * 32 + k;
+      const float4* src = reinterpret_cast<const float4*>(
+          p.ws_O + ((size_t)(piece ? 2 * (c + piece) : 2 * c + 1) * kRows + row) * kMlaD + lane * 8);
+      const float4 a = src[0], b = src[1];
+      if (w > 0.0f) {
+        den = fmaf(w, lk, den);
+        acc[0] = fmaf(w, a.x, acc[0]);
+        acc[1] = fmaf(w, a.y, acc[1]);
+        acc[2] = fmaf(w, a.z, acc[2]);
+        acc[3] = fmaf(w, a.w, acc[3]);
+        acc[4] = fmaf(w, b.x, acc[4]);
+        acc[5] = fmaf(w, b.y, acc[5]);
+        acc[6] = fmaf(w, b.z, acc[6]);
+        acc[7] = fmaf(w, b.w, acc[7]);
+      }
+    }
+  }
+  const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+  const size_t orow = (size_t)(meta[2] + tok) * p.Hq + (meta[4] << p.g_log2) + (row & ((1 << p.g_log2) - 1));
+  uint4 v;
+  v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+  v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+  v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
+  reinterpret_cast<uint4*>(p.O + orow * kMlaD)[lane] = v;
+  if (p.lse && lane == 0) p.lse[orow] = den > 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
+}
+
+// Pairs of a launch: one per two SMs of the current device.
+int pairs_of_device() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!cache[dev]) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+      return 0;
+    cache[dev] = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+  }
+  return cache[dev];
+}
+
+constexpr size_t kPieceBytes = (size_t)kRows * kMlaD * 4 + 2 * kRows * 4;
+
+size_t workspace_bytes_of(int pairs) { return (size_t)pairs * (2 * kPieceBytes + kMetaInts * 4); }
 
 }  // namespace
 }  // namespace hcadsa
 
 extern "C" size_t mla_paged_attn_fwd_workspace_size(int B, int T, int Hq, int Hkv) {
-  (void)B;
-  (void)T;
-  (void)Hq;
-  (void)Hkv;
-  return 0;
+  using namespace hcadsa;
+  if (B <= 0 || T <= 0 || Hkv <= 0 || check_query_sizes(T, Hq, Hkv, kMlaD, 1.0f) != HCADSA_OK) return 0;
+  return workspace_bytes_of(pairs_of_device());
 }
 
 extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,
@@ -115,19 +701,40 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
       !aligned4(cu_q) || !aligned4(kv_len) || !aligned4(lse))
     return HCADSA_ERR_ALIGN;
   if (B == 0 || T == 0) return HCADSA_OK;
+  const int pairs = pairs_of_device();
+  if (pairs <= 0) return HCADSA_ERR_CUDA;
+  if (!workspace || workspace_bytes < workspace_bytes_of(pairs)) return HCADSA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return HCADSA_ERR_ALIGN;
   Params p;
   p.s = paged_batch(table, cu_q, kv_len, B, T, n_pages, page, max_pages);
-  p.Q = Q;
-  p.K_pool = K_pool;
-  p.V_pool = V_pool;
   p.O = O;
   p.lse = lse;
-  p.q_row = q_row_stride;
-  p.k_page = k_page_stride;
-  p.v_page = v_page_stride;
+  p.ws_O = static_cast<float*>(workspace);
+  p.ws_ml = p.ws_O + (size_t)2 * pairs * kRows * kMlaD;
+  p.ws_meta = reinterpret_cast<int*>(p.ws_ml + (size_t)2 * pairs * 2 * kRows);
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.scale = scale;
-  attn_kernel<<<dim3(T, (Hq + 7) / 8 < 8 ? (Hq + 7) / 8 : 8), 256, 0, as_stream(stream)>>>(p);
+  p.g_log2 = log2_of(Hq / Hkv);
+  p.box_log2 = page < 64 ? log2_of(page) : 6;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  CUtensorMap mq, mk, mv;
+  {
+    const int g = 1 << p.g_log2;
+    const uint64_t dims[3] = {(uint64_t)kMlaD, (uint64_t)Hq, (uint64_t)T};
+    const uint64_t strides[2] = {(uint64_t)kMlaD * 2, (uint64_t)q_row_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)g, (uint32_t)(128 / g)};
+    if (!encode_tmap_bf16(&mq, 3, const_cast<hcadsa_bf16*>(Q), dims, strides, box, true)) return HCADSA_ERR_CUDA;
+  }
+  for (int v = 0; v < 2; ++v) {
+    const uint64_t dims[4] = {(uint64_t)kMlaD, (uint64_t)Hkv, (uint64_t)page, (uint64_t)n_pages};
+    const uint64_t strides[3] = {(uint64_t)kMlaD * 2, (uint64_t)Hkv * kMlaD * 2,
+                                 (uint64_t)(v ? v_page_stride : k_page_stride) * 2};
+    const uint32_t box[4] = {64, 1, 1u << p.box_log2, 1};
+    if (!encode_tmap_bf16(v ? &mv : &mk, 4, const_cast<hcadsa_bf16*>(v ? V_pool : K_pool), dims, strides, box, true))
+      return HCADSA_ERR_CUDA;
+  }
+  attn_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, mv, p);
+  HCADSA_TRY(launch_status());
+  combine_kernel<<<dim3(pairs, kRows / kCombineWarps), 32 * kCombineWarps, 0, as_stream(stream)>>>(p, pairs);
   return launch_status();
 }
