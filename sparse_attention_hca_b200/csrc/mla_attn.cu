@@ -15,9 +15,8 @@
 //   S  = Q (A, smem) * K^T (B, smem, K-major)        128 columns of TMEM, two buffers
 //   O += P (A, TMEM, bf16 over its own S) * V (B, smem, MN-major)   256 columns of TMEM
 // S and O together are all 512 columns.  Roles per CTA: warp 0 TMA (both CTAs; the lanes issue a
-// tile's page boxes side by side), warp 1 the MMA thread (leader CTA), warps 4-7 softmax, one
-// thread per row: the whole row of a tile is in registers, so its maximum and sum need no
-// exchange.  The reference maximum moves only when it is exceeded by 2^8 (lazy rescale of O).
+// tile's page boxes side by side), warp 1 the MMA thread (leader CTA), warps 4-11 softmax, two
+// threads per row.  The reference maximum moves only when it is exceeded by 2^8 (lazy rescale of O).
 //
 // Schedule: the (row tile, key tile) products of the whole batch form one list -- sequence, K/V
 // head, row tile, key tile -- whose length follows in closed form from the lengths.  Pair c of G
@@ -45,7 +44,8 @@ constexpr int kSlotBytes = 32 * 1024;      // K: 64 rows x 256, or V: 128 rows x
 constexpr int kQBytes = 64 * 1024;         // 128 rows x 256
 constexpr int kQChunk = 16 * 1024, kKChunk = 8 * 1024, kVChunk = 16 * 1024;  // 64 columns of each
 constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
-constexpr int kThreads = 256;
+constexpr int kSoftmaxWarps = 8;           // two per TMEM lane quarter: each takes half of a row
+constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr uint32_t kTmemS = 256;           // S buffers at columns 256 and 384; O at 0
 constexpr float kLazyRescale = 8.0f;
 constexpr int kMetaInts = 8;
@@ -265,7 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.p_ready[s], 8);  // the softmax warps of both CTAs
+      mbar_init(&bar.p_ready[s], 2 * kSoftmaxWarps);  // the softmax warps of both CTAs
     }
     mbar_init(&bar.pv_done, 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar.v_tail[s], 1);
@@ -405,12 +405,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax and output (one thread per row)
-    const int quarter = warp & 3;
-    const int row = (int)rank * 128 + quarter * 32 + lane;  // row of the row tile
+    // ------------------------------------------------------------ softmax and output
+    // Two threads per row, lanes t and t + 16 of one warp (16 TMEM lanes of its quarter): half hf
+    // takes keys 64 hf .. +63 of a tile and columns 128 hf .. +127 of the output.
+    const int lane0 = (warp & 3) * 32 + ((warp - 4) >> 2) * 16, hf = lane >> 4;
+    const int row = (int)rank * 128 + lane0 + (lane & 15);  // row of the row tile
     const int my_tok = row >> p.g_log2, my_head = row & ((1 << p.g_log2) - 1);
-    const uint32_t t_lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int tid = quarter * 32 + lane;
+    const uint32_t t_lanes = tmem + (static_cast<uint32_t>(lane0) << 16);
+    const int tid = threadIdx.x - 128;
     uint32_t g = 0, u = 0, tails = 0;
     bool ok = true;
     int head_flag = 0, tail_flag = 0, tail_tok = 0, tail_n = 0, tail_h = 0;  // for ws_meta
@@ -419,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int tok = w.first_token() + my_tok;  // token of the sequence
       const bool valid = tok < w.q.n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
-      const int n_vis = min(w.q.base + tok + 1, w.q.len);  // rows this row sees (may be <= 0)
+      const int n_vis = min(w.q.base + tok + 1, w.q.len) - 64 * hf;  // rows this row sees (may be <= 0)
       float m_run = -INFINITY, l_run = 0.0f;
       for (int jj = 0; jj < J; ++jj, ++g) {
         const int j = w.j0 + jj;
@@ -427,25 +429,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (warp_valid) {
           const uint32_t tS = t_lanes + kTmemS + (g & 1) * kKeyTile;
-          uint32_t s[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + c * 32, s[c]);
+          uint32_t s[2][32];
+          tmem_ld_half32<64>(tS, s[0]);
+          tmem_ld_half32<64>(tS + 32, s[1]);
           tmem_wait_ld_regs2(s[0], s[1]);
-          tmem_wait_ld_regs2(s[2], s[3]);
           const int vis = n_vis - j * kKeyTile;
-          if (!__all_sync(0xffffffffu, vis >= kKeyTile)) {
+          if (!__all_sync(0xffffffffu, vis >= 64)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int x = 0; x < 32; ++x)
                 if (c * 32 + x >= vis) s[c][x] = 0xff800000u;
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
+          for (int x = 0; x < 16; ++x)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(s[c][x]));
-          const float xt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(s[c >> 1][2 * x + (c & 1)]));
+          const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float xt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16)) * p.scale_log2;
           bool resc = false;
           float alpha = 1.0f;
           if (m_run == -INFINITY) {
@@ -459,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           l_run *= alpha;
           float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t pw[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
@@ -469,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               l4[(2 * x + 1) & 3] += p1;
               pw[x] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(tS + c * 16, pw);
+            tmem_st_half16<32>(tS + c * 16, pw);
           }
           l_run += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           if (__any_sync(0xffffffffu, resc)) {
@@ -477,13 +479,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = mbar_wait(&bar.pv_done, (g - 1) & 1, &abort_flag, p.s.err) && ok;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
-              tmem_ld32_nowait(t_lanes + c * 32, o);
+              tmem_ld_half32<128>(t_lanes + c * 32, o);
               tmem_wait_ld_regs(o);
 #pragma unroll
               for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-              tmem_st32(t_lanes + c * 32, o);
+              tmem_st_half32<128>(t_lanes + c * 32, o);
             }
           }
           tmem_wait_st();
@@ -494,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++tails;
           const int r0 = w.q.len & (kKeyTile - 1), r1 = (r0 + box_rows - 1) & ~(box_rows - 1);
           uint8_t* slot = sRing + ((u + 2 * J - 1) % kSlots) * kSlotBytes;
-          for (int e = tid; e < (r1 - r0) * 16; e += 128) {
+          for (int e = tid; e < (r1 - r0) * 16; e += 32 * kSoftmaxWarps) {
             const int r = r0 + (e >> 4), x = e & 15;
             *reinterpret_cast<uint4*>(slot + (x >> 3) * kVChunk + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -513,24 +515,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = w.j0 == 0 && w.j1 == w.n_keys;
       if (warp_valid) {
+        const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
         const size_t orow = (size_t)(w.q.q0 + tok) * p.Hq + (w.h << p.g_log2) + my_head;
-        const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         const int slot = 2 * pair + (w.j0 == 0 ? 1 : 0);
-        if (valid) {
+        if (valid && hf == 0) {
           if (whole) {
-            if (p.lse) p.lse[orow] = l_run > 0.0f ? (m_run + __log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            if (p.lse) p.lse[orow] = l > 0.0f ? (m_run + __log2f(l)) * 0.69314718055994531f : -INFINITY;
           } else {
             p.ws_ml[(size_t)slot * 2 * kRows + row] = m_run;
-            p.ws_ml[(size_t)slot * 2 * kRows + kRows + row] = l_run;
+            p.ws_ml[(size_t)slot * 2 * kRows + kRows + row] = l;
           }
         }
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
-          tmem_ld32_nowait(t_lanes + c * 32, o);
+          tmem_ld_half32<128>(t_lanes + c * 32, o);
           tmem_wait_ld_regs(o);
           if (valid && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.O + orow * kMlaD + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.O + orow * kMlaD + hf * 128 + c * 32);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               uint4 v;
@@ -541,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               dst[x] = v;
             }
           } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * kRows + row) * kMlaD + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * kRows + row) * kMlaD + hf * 128 + c * 32);
 #pragma unroll
             for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
