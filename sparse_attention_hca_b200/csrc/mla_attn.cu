@@ -388,7 +388,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (step >= 1) {
             const uint32_t gj = g + step - 1, s = u % kSlots;
             ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err) &&
-                 mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err);
+                 (is_tail(w.q.len, w.j0 + step - 1)
+                      ? mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err)
+                      : mbar_wait(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err));
             if (!ok) break;
             tc_fence_after();
             const uint32_t tP = tmem + kTmemS + (gj & 1) * kKeyTile;  // bf16 pairs: 64 columns
@@ -490,7 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        if (is_tail(w.q.len, j)) {
+        const bool tail = is_tail(w.q.len, j);
+        if (tail) {
           // V of the piece's last tile: clear the rows behind the sequence's end, up to the box's end
           ok = mbar_wait(&bar.v_tail[tails & 1], (tails >> 1) & 1, &abort_flag, p.s.err) && ok;
           ++tails;
@@ -504,7 +507,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(cluster_addr(&bar.p_ready[g & 1], 0));
+        if (lane == 0) {
+          const uint32_t ready = cluster_addr(&bar.p_ready[g & 1], 0);
+          if (tail) arrive_cluster(ready);
+          else arrive_cluster_tmem(ready);
+        }
       }
       u += 2 * J;
       // ---- output of the piece, once its last PV is done.  The last tile's scores only showed that
