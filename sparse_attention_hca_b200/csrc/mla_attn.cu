@@ -38,11 +38,11 @@ namespace hcadsa {
 namespace {
 
 constexpr int kKeyTile = 128;
-constexpr int kRows = 256;                 // (token, head) rows of a row tile
-constexpr int kSlots = 5;                  // ring of K and V half tiles
-constexpr int kSlotBytes = 32 * 1024;      // K: 64 rows x 256, or V: 128 rows x 128
+constexpr int kCtaRows = 128;              // (token, head) rows of a CTA: TMEM lanes
+constexpr int kSlots = 5;                  // ring of half tiles of K and V
+constexpr int kSlotBytes = 32 * 1024;
 constexpr int kQBytes = 64 * 1024;         // 128 rows x 256
-constexpr int kQChunk = 16 * 1024, kKChunk = 8 * 1024, kVChunk = 16 * 1024;  // 64 columns of each
+constexpr int kQChunk = 16 * 1024;         // 64 columns of 128 rows
 constexpr int kSmemBytes = kQBytes + kSlots * kSlotBytes + 1024;
 constexpr int kSoftmaxWarps = 8;           // two per TMEM lane quarter: each takes half of a row
 constexpr int kThreads = 128 + 32 * kSoftmaxWarps;
@@ -54,11 +54,26 @@ struct Params {
   PagedBatch s;
   uint16_t* O;
   float* lse;
-  float* ws_O;   // [2 G][256][256]: pair c's piece that began before its range (2 c) and after (2 c + 1)
-  float* ws_ml;  // [2 G][2][256]: reference maximum (log2 units), sum
+  float* ws_O;   // [2 G][rows][256]: worker c's piece that began before its range (2 c) or in it (2 c + 1)
+  float* ws_ml;  // [2 G][2][rows]: reference maximum (log2 units), sum
   int* ws_meta;  // [G][kMetaInts]
   int Hq, Hkv, g_log2, box_log2;
   float scale_log2;
+};
+
+// A worker is a CTA pair or a single CTA.
+//   pair   : row tile 256 rows; a slot is CTA r's half of a tile for the pair's MMAs: K rows 64 r .. +63
+//            (4 chunks of 64 columns), V columns 128 r .. +127 (2 chunks of 128 rows)
+//   single : row tile 128 rows; a tile is two slots: K columns 128 half .. +127 (2 chunks of 128 rows),
+//            V rows 64 half .. +63 (4 chunks of 64 rows)
+template <bool kPair>
+struct Shape {
+  static constexpr int kRows = kPair ? 2 * kCtaRows : kCtaRows;
+  static constexpr int kRowsLog2 = kPair ? 8 : 7;
+  static constexpr int kParts = kPair ? 1 : 2;                           // slots of a tile
+  static constexpr int kKChunk = kPair ? 8 * 1024 : 16 * 1024;           // bytes of a slot's 64 columns
+  static constexpr int kVChunk = kPair ? 16 * 1024 : 8 * 1024;
+  static constexpr int kReady = (kPair ? 2 : 1) * kSoftmaxWarps;
 };
 
 struct __align__(8) Barriers {
@@ -126,11 +141,12 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2) {
 }
 
 struct Start {
-  long long count;  // products of this pair
+  long long count;  // products of this worker
   int b, h, i, j;   // where they begin
 };
 
-// Walks a pair's pieces: runs of key tiles of one row tile.
+// Walks a worker's pieces: runs of key tiles of one row tile.
+template <int kRowsLog2>
 struct Walk {
   const Params& p;
   long long left;
@@ -138,7 +154,7 @@ struct Walk {
   PagedSeq q;
   SeqTiles t;
   __device__ Walk(const Params& p_, const Start& s) : p(p_) {
-    tq_log2 = 8 - p.g_log2;
+    tq_log2 = kRowsLog2 - p.g_log2;
     left = s.count;
     b = s.b;
     h = s.h;
@@ -184,11 +200,10 @@ struct Walk {
   }
 };
 
-// Every thread of the CTA: this pair's share of the list.
-__device__ __forceinline__ void find_start(const Params& p, int pair, int n_pairs, Start* out) {
+// Every thread of the CTA: this worker's share of the list.
+__device__ __forceinline__ void find_start(const Params& p, int tq_log2, int worker, int n_workers, Start* out) {
   __shared__ long long sums[kThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tq_log2 = 8 - p.g_log2;
   auto work_of = [&](int b, bool report) -> long long {
     if (b >= p.s.B) return 0;
     const SeqTiles t = seq_tiles(paged_seq(p.s, b, report), tq_log2);
@@ -215,10 +230,10 @@ __device__ __forceinline__ void find_start(const Params& p, int pair, int n_pair
   long long mine = 0, all;
   for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
   scan(mine, all);
-  // a short list goes to as many pairs as it has products, so that consecutive pieces of a row
-  // tile always lie in consecutive pairs
-  const int n = all < n_pairs ? (int)all : n_pairs;
-  const long long lo = pair < n ? all * pair / n : 0, hi = pair < n ? all * (pair + 1) / n : 0;
+  // a short list goes to as many workers as it has products, so that consecutive pieces of a row
+  // tile always lie with consecutive workers
+  const int n = all < n_workers ? (int)all : n_workers;
+  const long long lo = worker < n ? all * worker / n : 0, hi = worker < n ? all * (worker + 1) / n : 0;
   if (tid == 0) out->count = hi - lo;
   long long done = 0;
   for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
@@ -242,7 +257,21 @@ __device__ __forceinline__ void find_start(const Params& p, int pair, int n_pair
 
 // ------------------------------------------------------------------ the kernel
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kPair) mma_commit_pair(bar);
+  else mma_commit(bar);
+}
+// A page box into this CTA's shared memory, completing on the leader's copy of `bar`.
+template <bool kPair>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int col, int head, int row,
+                                         int page) {
+  if constexpr (kPair) tma_load_4d_pair(dst, map, cluster_addr(bar, 0), col, head, row, page);
+  else tma_load_4d(dst, map, bar, col, head, row, page);
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -254,8 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_rank();  // 0: the leader, which issues the MMAs
-  const int pair = (int)blockIdx.x >> 1, n_pairs = (int)gridDim.x >> 1;
+  using Sh = Shape<kPair>;
+  using Pieces = Walk<Sh::kRowsLog2>;
+  const uint32_t rank = kPair ? cluster_rank() : 0;  // 0: the leader, which issues the MMAs
+  const int worker = kPair ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+  const int n_workers = kPair ? (int)gridDim.x >> 1 : (int)gridDim.x;
   if (threadIdx.x == 0) {
     mbar_init(&bar.q_full, 1);
     mbar_init(&bar.q_empty, 1);
@@ -265,142 +297,195 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bar.s_full[s], 1);
-      mbar_init(&bar.p_ready[s], 2 * kSoftmaxWarps);  // the softmax warps of both CTAs
+      mbar_init(&bar.p_ready[s], Sh::kReady);  // the worker's softmax warps
     }
     mbar_init(&bar.pv_done, 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar.v_tail[s], 1);
     abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 1) tmem_alloc_pair(&tmem_base_sh, 512);
-  find_start(p, pair, n_pairs, &start);
+  if (warp == 1) {
+    if constexpr (kPair) {
+      tmem_alloc_pair(&tmem_base_sh, 512);
+    } else {
+      tmem_alloc(&tmem_base_sh, 512);
+      tmem_relinquish();
+    }
+  }
+  find_start(p, Sh::kRowsLog2 - p.g_log2, worker, n_workers, &start);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
+  if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const int box_rows = 1 << p.box_log2;
   // whether key tile j holds rows behind the sequence's end that a page box brings in
   auto is_tail = [&](int len, int j) { return (len & (box_rows - 1)) != 0 && len / kKeyTile == j; };
+  // the half of such a tile (64 rows) that holds them: a box lies in one half
+  auto tail_part = [](int len) { return (len & (kKeyTile - 1)) >> 6; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (all lanes)
-    const int n_tma = 256 >> p.box_log2;  // boxes of a half tile: K 64 / box rows x 4 chunks, V 128 / box rows x 2
-    const int kbox = lane >> 2, kchunk = lane & 3, vbox = lane >> 1, vchunk = lane & 1;
+    // A slot is 256 / box rows page boxes, one per lane: `wide` slots (128 rows x 2 chunks) and
+    // `narrow` ones (64 rows x 4 chunks); a pair's K and a single CTA's V are narrow.
+    const int n_tma = 256 >> p.box_log2;
+    const int nrow = (lane >> 2) << p.box_log2, nchunk = lane & 3, wrow = (lane >> 1) << p.box_log2, wchunk = lane & 1;
+    const int k_row = kPair ? nrow + 64 * (int)rank : wrow;  // this lane's row of a K tile
+    const int v_row = kPair ? wrow : nrow;                   // and of a V tile (single: + 64 per part)
     const int page_mask = (1 << p.s.page_log2) - 1;
-    uint32_t u = 0;  // half tiles issued: slot u % kSlots
+    uint32_t u = 0;  // slots issued: slot u % kSlots
     uint32_t it = 0, tails = 0;
     bool ok = true;
-    for (Walk w(p, start); !w.done() && ok; w.next(), ++it) {
+    for (Pieces w(p, start); !w.done() && ok; w.next(), ++it) {
       const int J = w.tiles();
       auto page_of = [&](int row) -> int {  // a page that is not there: zeros (outside the tensor map)
         if (lane >= n_tma || row >= w.q.len) return p.s.n_pages;
         const int pg = paged_page(p.s, w.b, row);
         return pg < 0 ? p.s.n_pages : pg;
       };
+      auto wait_slot = [&]() -> bool {
+        return __all_sync(0xffffffffu,
+                          mbar_wait(&bar.empty[u % kSlots], ((u / kSlots) & 1) ^ 1, &abort_flag, p.s.err));
+      };
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.q_empty, (it & 1) ^ 1, &abort_flag, p.s.err));
       if (!ok) break;
       if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(&bar.q_full, 2 * kQBytes);
-        const uint32_t full = cluster_addr(&bar.q_full, 0);
+        if (rank == 0) mbar_arrive_expect_tx(&bar.q_full, (kPair ? 2 : 1) * kQBytes);
         const int tok = w.q.q0 + w.first_token() + (int)(rank << (7 - p.g_log2));
-        for (int c = 0; c < 4; ++c)
-          tma_load_3d_pair(sQ + c * kQChunk, &map_q, full, c * 64, w.h << p.g_log2, tok);
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (kPair)
+            tma_load_3d_pair(sQ + c * kQChunk, &map_q, cluster_addr(&bar.q_full, 0), c * 64, w.h << p.g_log2, tok);
+          else
+            tma_load_3d(sQ + c * kQChunk, &map_q, &bar.q_full, c * 64, w.h << p.g_log2, tok);
+        }
       }
       __syncwarp();
-      int pk = page_of(w.j0 * kKeyTile + 64 * (int)rank + (kbox << p.box_log2)), pv = 0;
+      // the pages of the next K tile, and of a K tile's V (used a step later), are looked up ahead
+      int pk = page_of(w.j0 * kKeyTile + k_row), pv[Sh::kParts] = {};
       for (int step = 0; step <= J && ok; ++step) {
         const int j = w.j0 + step;
-        // the pages of the next K tile and of this step's V tile of the next step are looked up ahead
-        int pk_next = 0, pv_next = 0;
-        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + 64 * (int)rank + (kbox << p.box_log2));
-        if (step < J) pv_next = page_of(j * kKeyTile + (vbox << p.box_log2));
+        int pk_next = 0, pv_next[Sh::kParts] = {};
+        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + k_row);
         if (step < J) {
-          const uint32_t s = u % kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], ((u / kSlots) & 1) ^ 1, &abort_flag, p.s.err));
-          if (!ok) break;
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kSlotBytes);
-          __syncwarp();
-          if (lane < n_tma) {
-            const int row = j * kKeyTile + 64 * (int)rank + (kbox << p.box_log2);
-            tma_load_4d_pair(sRing + s * kSlotBytes + kchunk * kKChunk + (kbox << p.box_log2) * 128, &map_k,
-                             cluster_addr(&bar.full[s], 0), kchunk * 64, w.h, row & page_mask, pk);
+#pragma unroll
+          for (int part = 0; part < Sh::kParts; ++part)
+            pv_next[part] = page_of(j * kKeyTile + v_row + 64 * part);
+#pragma unroll
+          for (int part = 0; part < Sh::kParts && ok; ++part) {
+            ok = wait_slot();
+            if (!ok) break;
+            const uint32_t s = u % kSlots;
+            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], (kPair ? 2 : 1) * kSlotBytes);
+            __syncwarp();
+            if (lane < n_tma) {
+              uint8_t* dst = sRing + s * kSlotBytes;
+              if constexpr (kPair)
+                load_box<true>(dst + nchunk * Sh::kKChunk + nrow * 128, &map_k, &bar.full[s], nchunk * 64, w.h,
+                               (j * kKeyTile + k_row) & page_mask, pk);
+              else
+                load_box<false>(dst + wchunk * Sh::kKChunk + wrow * 128, &map_k, &bar.full[s],
+                                (2 * part + wchunk) * 64, w.h, (j * kKeyTile + k_row) & page_mask, pk);
+            }
+            ++u;
           }
-          ++u;
         }
         if (step >= 1) {
-          const uint32_t s = u % kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar.empty[s], ((u / kSlots) & 1) ^ 1, &abort_flag, p.s.err));
-          if (!ok) break;
-          const int row = (j - 1) * kKeyTile + (vbox << p.box_log2);
-          uint8_t* dst = sRing + s * kSlotBytes + vchunk * kVChunk + (vbox << p.box_log2) * 128;
-          const int col = 128 * (int)rank + vchunk * 64;
-          if (is_tail(w.q.len, j - 1)) {
-            uint64_t* tail = &bar.v_tail[tails++ & 1];
-            if (lane == 0) {
-              mbar_arrive_expect_tx(tail, kSlotBytes);
-              if (rank == 0) mbar_arrive(&bar.full[s]);
+          const bool tail_tile = is_tail(w.q.len, j - 1);
+#pragma unroll
+          for (int part = 0; part < Sh::kParts && ok; ++part) {
+            ok = wait_slot();
+            if (!ok) break;
+            const uint32_t s = u % kSlots;
+            const int in = ((j - 1) * kKeyTile + v_row + 64 * part) & page_mask;
+            uint8_t* dst = sRing + s * kSlotBytes +
+                           (kPair ? wchunk * Sh::kVChunk + wrow * 128 : nchunk * Sh::kVChunk + nrow * 128);
+            const int col = kPair ? 128 * (int)rank + wchunk * 64 : nchunk * 64;
+            if (tail_tile && (kPair || part == tail_part(w.q.len))) {
+              uint64_t* tail = &bar.v_tail[tails++ & 1];
+              if (lane == 0) {
+                mbar_arrive_expect_tx(tail, kSlotBytes);
+                if (rank == 0) mbar_arrive(&bar.full[s]);
+              }
+              __syncwarp();
+              if (lane < n_tma) tma_load_4d(dst, &map_v, tail, col, w.h, in, pv[part]);
+            } else {
+              if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], (kPair ? 2 : 1) * kSlotBytes);
+              __syncwarp();
+              if (lane < n_tma) load_box<kPair>(dst, &map_v, &bar.full[s], col, w.h, in, pv[part]);
             }
-            __syncwarp();
-            if (lane < n_tma) tma_load_4d(dst, &map_v, tail, col, w.h, row & page_mask, pv);
-          } else {
-            if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], 2 * kSlotBytes);
-            __syncwarp();
-            if (lane < n_tma)
-              tma_load_4d_pair(dst, &map_v, cluster_addr(&bar.full[s], 0), col, w.h, row & page_mask, pv);
+            ++u;
           }
-          ++u;
         }
         pk = pk_next;
-        pv = pv_next;
+#pragma unroll
+        for (int part = 0; part < Sh::kParts; ++part) pv[part] = pv_next[part];
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader)
     if (lane == 0 && rank == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeyTile, false, false);
-      const uint32_t idesc_o = idesc_bf16_f32(kRows, kMlaD, false, true);
+      const uint32_t idesc_s = idesc_bf16_f32(Sh::kRows, kKeyTile, false, false);
+      const uint32_t idesc_o = idesc_bf16_f32(Sh::kRows, kMlaD, false, true);
       const uint32_t sQa = smem_u32(sQ), sRa = smem_u32(sRing);
       const uint64_t dq = smem_desc_sw128(sQa, 16, 1024);
       uint32_t u = 0, it = 0, g = 0;  // g: key tiles so far (S buffer and barrier phases)
       bool ok = true;
-      for (Walk w(p, start); !w.done() && ok; w.next(), ++it) {
+      for (Pieces w(p, start); !w.done() && ok; w.next(), ++it) {
         const int J = w.tiles();
         ok = mbar_wait(&bar.q_full, it & 1, &abort_flag, p.s.err);
         for (int step = 0; step <= J && ok; ++step) {
           if (step < J) {
-            const uint32_t gs = g + step, s = u % kSlots;
-            ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+            const uint32_t gs = g + step, tS = tmem + kTmemS + (gs & 1) * kKeyTile;
+#pragma unroll
+            for (int part = 0; part < Sh::kParts && ok; ++part) {
+              const uint32_t s = u % kSlots;
+              ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, 1024);
+#pragma unroll
+              for (int c = 0; c < 4 / Sh::kParts; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {  // start addresses in 16-byte units
+                  const uint64_t a = dq + (uint64_t)(((part * 2 + c) * kQChunk + kk * 32) >> 4);
+                  const uint64_t b = dk + (uint64_t)((c * Sh::kKChunk + kk * 32) >> 4);
+                  if constexpr (kPair) mma_ss_pair(tS, a, b, idesc_s, (part | c | kk) != 0);
+                  else mma_ss(tS, a, b, idesc_s, (part | c | kk) != 0);
+                }
+              commit<kPair>(&bar.empty[s]);
+              ++u;
+            }
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, 1024);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
-                mma_ss_pair(tmem + kTmemS + (gs & 1) * kKeyTile, dq + (uint64_t)((c * kQChunk + kk * 32) >> 4),
-                            dk + (uint64_t)((c * kKChunk + kk * 32) >> 4), idesc_s, (c | kk) != 0);
-            mma_commit_pair(&bar.empty[s]);
-            mma_commit_pair(&bar.s_full[gs & 1]);
-            if (step == J - 1) mma_commit_pair(&bar.q_empty);
-            ++u;
+            commit<kPair>(&bar.s_full[gs & 1]);
+            if (step == J - 1) commit<kPair>(&bar.q_empty);
           }
           if (step >= 1) {
-            const uint32_t gj = g + step - 1, s = u % kSlots;
-            ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err) &&
-                 (is_tail(w.q.len, w.j0 + step - 1)
-                      ? mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err)
-                      : mbar_wait(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err));
-            if (!ok) break;
-            tc_fence_after();
+            const uint32_t gj = g + step - 1;
             const uint32_t tP = tmem + kTmemS + (gj & 1) * kKeyTile;  // bf16 pairs: 64 columns
-            const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, kVChunk, 1024);
 #pragma unroll
-            for (int kk = 0; kk < kKeyTile / 16; ++kk)
-              mma_ts_pair(tmem, tP + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), idesc_o, (step > 1 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(&bar.empty[s]);
-            mma_commit_pair(&bar.pv_done);
-            ++u;
+            for (int part = 0; part < Sh::kParts && ok; ++part) {
+              const uint32_t s = u % kSlots;
+              ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+              if (ok && part == 0)
+                ok = kPair && is_tail(w.q.len, w.j0 + step - 1)
+                         ? mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err)
+                         : mbar_wait(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, Sh::kVChunk, 1024);
+#pragma unroll
+              for (int kk = 0; kk < kKeyTile / 16 / Sh::kParts; ++kk) {
+                const uint32_t a = tP + (part * 4 + kk) * 8;
+                const uint64_t b = dv + (uint64_t)((kk * 2048) >> 4);
+                const uint32_t acc = (step > 1 || part > 0 || kk > 0) ? 1u : 0u;
+                if constexpr (kPair) mma_ts_pair(tmem, a, b, idesc_o, acc);
+                else mma_ts(tmem, a, b, idesc_o, acc);
+              }
+              commit<kPair>(&bar.empty[s]);
+              ++u;
+            }
+            if (!ok) break;
+            commit<kPair>(&bar.pv_done);
           }
         }
         g += J;
@@ -418,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t g = 0, u = 0, tails = 0;
     bool ok = true;
     int head_flag = 0, tail_flag = 0, tail_tok = 0, tail_n = 0, tail_h = 0;  // for ws_meta
-    for (Walk w(p, start); !w.done(); w.next()) {
+    for (Pieces w(p, start); !w.done(); w.next()) {
       const int J = w.tiles();
       const int tok = w.first_token() + my_tok;  // token of the sequence
       const bool valid = tok < w.q.n;
@@ -498,22 +583,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&bar.v_tail[tails & 1], (tails >> 1) & 1, &abort_flag, p.s.err) && ok;
           ++tails;
           const int r0 = w.q.len & (kKeyTile - 1), r1 = (r0 + box_rows - 1) & ~(box_rows - 1);
-          uint8_t* slot = sRing + ((u + 2 * J - 1) % kSlots) * kSlotBytes;
-          for (int e = tid; e < (r1 - r0) * 16; e += 32 * kSoftmaxWarps) {
-            const int r = r0 + (e >> 4), x = e & 15;
-            *reinterpret_cast<uint4*>(slot + (x >> 3) * kVChunk + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          const int part = kPair ? 0 : tail_part(w.q.len);
+          constexpr int kRowPieces = kPair ? 16 : 32;  // 16-byte pieces of a row in the slot
+          uint8_t* slot = sRing + ((u + (2 * J - 1) * Sh::kParts + part) % kSlots) * kSlotBytes;
+          for (int e = tid; e < (r1 - r0) * kRowPieces; e += 32 * kSoftmaxWarps) {
+            const int r = r0 + e / kRowPieces - 64 * part, x = e % kRowPieces;
+            *reinterpret_cast<uint4*>(slot + (x >> 3) * Sh::kVChunk + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          const uint32_t ready = cluster_addr(&bar.p_ready[g & 1], 0);
-          if (tail) arrive_cluster(ready);
-          else arrive_cluster_tmem(ready);
+          if constexpr (kPair) {
+            const uint32_t ready = cluster_addr(&bar.p_ready[g & 1], 0);
+            if (tail) arrive_cluster(ready);
+            else arrive_cluster_tmem(ready);
+          } else {
+            mbar_arrive(&bar.p_ready[g & 1]);
+          }
         }
       }
-      u += 2 * J;
+      u += 2 * J * Sh::kParts;
       // ---- output of the piece, once its last PV is done.  The last tile's scores only showed that
       // the PV two tiles before it was: the one in between is waited for first, or its parity would
       // be taken for the last one's.
@@ -525,13 +616,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
         const size_t orow = (size_t)(w.q.q0 + tok) * p.Hq + (w.h << p.g_log2) + my_head;
         const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int slot = 2 * pair + (w.j0 == 0 ? 1 : 0);
+        const int slot = 2 * worker + (w.j0 == 0 ? 1 : 0);
         if (valid && hf == 0) {
           if (whole) {
             if (p.lse) p.lse[orow] = l > 0.0f ? (m_run + __log2f(l)) * 0.69314718055994531f : -INFINITY;
           } else {
-            p.ws_ml[(size_t)slot * 2 * kRows + row] = m_run;
-            p.ws_ml[(size_t)slot * 2 * kRows + kRows + row] = l;
+            p.ws_ml[(size_t)slot * 2 * Sh::kRows + row] = m_run;
+            p.ws_ml[(size_t)slot * 2 * Sh::kRows + Sh::kRows + row] = l;
           }
         }
 #pragma unroll 1
@@ -551,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               dst[x] = v;
             }
           } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * kRows + row) * kMlaD + hf * 128 + c * 32);
+            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * Sh::kRows + row) * kMlaD + hf * 128 + c * 32);
 #pragma unroll
             for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
@@ -570,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (rank == 0 && tid == 0) {
-      int* m = p.ws_meta + pair * kMetaInts;
+      int* m = p.ws_meta + worker * kMetaInts;
       m[0] = head_flag;
       m[1] = tail_flag;
       m[2] = tail_tok;
@@ -581,20 +672,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
+  if constexpr (kPair) cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) {
+    if constexpr (kPair) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
 }
 
-// Merges the pieces of a row tile that began in pair c's range and went on in pairs c+1, c+2, ...
-// (piece k >= 1 is the one pair c + k began with), in that order: with M the largest of the maxima,
+// Merges the pieces of a row tile that began in worker c's range and went on in those of workers
+// c+1, c+2, ... (piece k >= 1 is the one worker c + k began with), in that order: with M the largest
+// of the maxima,
 //     O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
 // One warp per row; the lanes read the pieces' (max, sum) side by side, so the loads of the rows
 // themselves (lane l: columns 8 l .. 8 l + 7) do not wait on one another.
 constexpr int kCombineWarps = 8;
-constexpr int kMaxPairs = 128;
+constexpr int kMaxWorkers = 160;
 
-__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p, int n_pairs) {
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p, int n_workers, int n_rows) {
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
   const int* meta = p.ws_meta + c * kMetaInts;
@@ -602,8 +697,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   const int tok = row >> p.g_log2;
   if (tok >= meta[3]) return;
   int n = 1;  // pieces
-  for (int k0 = c + 1; k0 < n_pairs; k0 += 32) {
-    const int flag = k0 + lane < n_pairs ? p.ws_meta[(k0 + lane) * kMetaInts] : 2;
+  for (int k0 = c + 1; k0 < n_workers; k0 += 32) {
+    const int flag = k0 + lane < n_workers ? p.ws_meta[(k0 + lane) * kMetaInts] : 2;
     const uint32_t last = __ballot_sync(0xffffffffu, flag != 1);
     if (last) {
       n += __ffs(last);
@@ -611,17 +706,17 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
     }
     n += 32;
   }
-  n = min(n, n_pairs - c);
-  float m[kMaxPairs / 32], l[kMaxPairs / 32], M = -INFINITY;
+  n = min(n, n_workers - c);
+  float m[kMaxWorkers / 32], l[kMaxWorkers / 32], M = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < kMaxPairs / 32; ++q) {
+  for (int q = 0; q < kMaxWorkers / 32; ++q) {
     const int k = q * 32 + lane;
     m[q] = -INFINITY;
     l[q] = 0.0f;
     if (k < n) {
-      const float* ml = p.ws_ml + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 * kRows + row;
+      const float* ml = p.ws_ml + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 * n_rows + row;
       m[q] = ml[0];
-      l[q] = ml[kRows];
+      l[q] = ml[n_rows];
     }
     if (l[q] > 0.0f) M = fmaxf(M, m[q]);
   }
@@ -629,7 +724,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float den = 0.0f, acc[8] = {};
 #pragma unroll
-  for (int q = 0; q < kMaxPairs / 32; ++q) {
+  for (int q = 0; q < kMaxWorkers / 32; ++q) {
     const float w_mine = l[q] > 0.0f ? exp2f(m[q] - M) : 0.0f;
     const int n_q = min(32, n - q * 32);
 #pragma unroll 4
@@ -637,7 +732,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
       const float w = __shfl_sync(0xffffffffu, w_mine, k), lk = __shfl_sync(0xffffffffu, l[q], k);
       const int piece = q * 32 + k;
       const float4* src = reinterpret_cast<const float4*>(
-          p.ws_O + ((size_t)(piece ? 2 * (c + piece) : 2 * c + 1) * kRows + row) * kMlaD + lane * 8);
+          p.ws_O + ((size_t)(piece ? 2 * (c + piece) : 2 * c + 1) * n_rows + row) * kMlaD + lane * 8);
       const float4 a = src[0], b = src[1];
       if (w > 0.0f) {
         den = fmaf(w, lk, den);
@@ -663,8 +758,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   if (p.lse && lane == 0) p.lse[orow] = den > 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Pairs of a launch: one per two SMs of the current device.
-int pairs_of_device() {
+// SMs of the current device, its kernels' shared memory set up.
+int sms_of_device() {
   static std::mutex mu;
   static int cache[64] = {};
   int dev = 0;
@@ -672,17 +767,50 @@ int pairs_of_device() {
   std::lock_guard<std::mutex> lock(mu);
   if (!cache[dev]) {
     int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (cudaFuncSetAttribute(attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2 ||
+        cudaFuncSetAttribute(attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(attn_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+            cudaSuccess) {
+      launch_status();
       return 0;
-    cache[dev] = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+    }
+    cache[dev] = sms < kMaxWorkers ? sms : kMaxWorkers;
   }
   return cache[dev];
 }
 
-constexpr size_t kPieceBytes = (size_t)kRows * kMlaD * 4 + 2 * kRows * 4;
+// The same for both kernels: half as many pairs, each with twice the rows.
+size_t workspace_bytes_of(int sms) {
+  return (size_t)sms * (2 * ((size_t)kCtaRows * kMlaD * 4 + 2 * kCtaRows * 4) + kMetaInts * 4);
+}
 
-size_t workspace_bytes_of(int pairs) { return (size_t)pairs * (2 * kPieceBytes + kMetaInts * 4); }
+// Pairs take row tiles of 256 rows and load half the K and V per product; single CTAs take row tiles
+// of 128 rows, so a sequence that has no more rows than that (a decode step) costs half the MMA time.
+// Both give right results for every batch; the host only knows the averages.
+bool use_pairs(int B, int T, int g) { return (long long)T * g > (long long)kCtaRows * B; }
+
+template <bool kPair>
+hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, int sms,
+                     cudaStream_t stream) {
+  const int workers = kPair ? sms / 2 : sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPair ? 2 * workers : workers, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
+  combine_kernel<<<dim3(workers, Shape<kPair>::kRows / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(
+      p, workers, Shape<kPair>::kRows);
+  return launch_status();
+}
 
 }  // namespace
 }  // namespace hcadsa
@@ -690,7 +818,7 @@ size_t workspace_bytes_of(int pairs) { return (size_t)pairs * (2 * kPieceBytes +
 extern "C" size_t mla_paged_attn_fwd_workspace_size(int B, int T, int Hq, int Hkv) {
   using namespace hcadsa;
   if (B <= 0 || T <= 0 || Hkv <= 0 || check_query_sizes(T, Hq, Hkv, kMlaD, 1.0f) != HCADSA_OK) return 0;
-  return workspace_bytes_of(pairs_of_device());
+  return workspace_bytes_of(sms_of_device());
 }
 
 extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,
@@ -711,17 +839,17 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
       !aligned4(cu_q) || !aligned4(kv_len) || !aligned4(lse))
     return HCADSA_ERR_ALIGN;
   if (B == 0 || T == 0) return HCADSA_OK;
-  const int pairs = pairs_of_device();
-  if (pairs <= 0) return HCADSA_ERR_CUDA;
-  if (!workspace || workspace_bytes < workspace_bytes_of(pairs)) return HCADSA_ERR_WORKSPACE;
+  const int sms = sms_of_device();
+  if (sms <= 0) return HCADSA_ERR_CUDA;
+  if (!workspace || workspace_bytes < workspace_bytes_of(sms)) return HCADSA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return HCADSA_ERR_ALIGN;
   Params p;
   p.s = paged_batch(table, cu_q, kv_len, B, T, n_pages, page, max_pages);
   p.O = O;
   p.lse = lse;
   p.ws_O = static_cast<float*>(workspace);
-  p.ws_ml = p.ws_O + (size_t)2 * pairs * kRows * kMlaD;
-  p.ws_meta = reinterpret_cast<int*>(p.ws_ml + (size_t)2 * pairs * 2 * kRows);
+  p.ws_ml = p.ws_O + (size_t)2 * sms * kCtaRows * kMlaD;
+  p.ws_meta = reinterpret_cast<int*>(p.ws_ml + (size_t)2 * sms * 2 * kCtaRows);
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.g_log2 = log2_of(Hq / Hkv);
@@ -743,8 +871,6 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
     if (!encode_tmap_bf16(v ? &mv : &mk, 4, const_cast<hcadsa_bf16*>(v ? V_pool : K_pool), dims, strides, box, true))
       return HCADSA_ERR_CUDA;
   }
-  attn_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, mv, p);
-  HCADSA_TRY(launch_status());
-  combine_kernel<<<dim3(pairs, kRows / kCombineWarps), 32 * kCombineWarps, 0, as_stream(stream)>>>(p, pairs);
-  return launch_status();
+  return use_pairs(B, T, Hq / Hkv) ? launch<true>(mq, mk, mv, p, sms, as_stream(stream))
+                                   : launch<false>(mq, mk, mv, p, sms, as_stream(stream));
 }
