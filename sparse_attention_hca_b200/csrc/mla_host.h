@@ -42,7 +42,7 @@ inline hcadsa_status check_row_stride(long long stride, int H) {
 inline hcadsa_status check_query_sizes(int T, int Hq, int Hkv, int d, float scale) {
   if (T < 0 || Hq <= 0 || Hq % Hkv || !(scale > 0.0f)) return HCADSA_ERR_SHAPE;
   const int g = Hq / Hkv;
-  if (d != kMlaD || g > 128 || (g & (g - 1))) return HCADSA_ERR_UNSUPPORTED;
+  if (d != kMlaD || g > 128 || (g & (g - 1)) || T > (1 << 23)) return HCADSA_ERR_UNSUPPORTED;
   return HCADSA_OK;
 }
 

@@ -1,71 +1,506 @@
 // mla_mass.cu -- the attention weight that every row of the paged cache of the full-context
-// (MLA) layers received from a chunk of new tokens (mla_paged_attn_mass).
+// (MLA) layers received from a chunk of new tokens (mla_paged_attn_mass), on sm_100a.
 //
 // Method: eviction keeps the rows that queries attended to, so each row accumulates
 //     mass[s] += sum over the chunk's tokens t that see s, and the query heads of the K/V head,
 //                of exp(scale <q[t], k_s> - lse[t])
 // with the log-sum-exp of the attention call.
 //
-// One warp per (row, K/V head), lane l holding channels 8 l .. 8 l + 7 of the key.
+// Tiles: keys are the M of the products.  A CTA pair holds 256 cache rows (CTA r the rows 128 r ..
+// +127, its TMEM lanes) and streams the chunk's (token, head) rows past them, 128 per tile (64 loaded
+// by each CTA): S^T = K (A) * Q^T (B), tcgen05 cta_group::2, M = 256, N = 128.  A thread owns a cache
+// row and sums exp2 over its TMEM lane's 128 columns: the sum over tokens and heads needs no exchange
+// between threads and no atomics.  Four S buffers (all of TMEM) decouple the MMAs from the sums; two
+// warpgroups take the tiles in turn.  The exponentials bound it: 128 x 128 of them per CTA and tile
+// take 1024 cycles on the SFUs, exactly what the MMAs take.
+// A decode step has few rows per sequence: the same Q tile stays in its slot from one block of cache
+// rows to the next, and the kernel streams K at HBM rate.
+//
+// Schedule: as the attention kernel's, one list of (256-row block, 128-row Q tile) products over the
+// batch -- sequence, K/V head, block, Q tile, those that see some row of the block -- cut evenly over
+// the pairs.  A block that several pairs share leaves partial sums in the workspace, which
+// add_kernel adds up in list order; every row's mass gets exactly one addition per call.
+#include <mutex>
+
 #include "mla_host.h"
+#include "pair.cuh"
 
 namespace hcadsa {
 namespace {
 
+constexpr int kKeys = 256;                  // cache rows of a block (128 per CTA)
+constexpr int kCols = 128;                  // (token, head) rows of a Q tile (64 loaded per CTA)
+constexpr int kKBytes = 64 * 1024, kKChunk = 16 * 1024;
+constexpr int kQSlots = 3, kQBytes = 32 * 1024, kQChunk = 8 * 1024;
+constexpr int kSmemBytes = 2 * kKBytes + kQSlots * kQBytes;
+constexpr int kThreads = 128 + 256;         // warp 0 TMA, warp 1 MMA, warps 4-11 sums
+constexpr int kMetaInts = 8;
+constexpr int kMaxPairs = 80;
+
 struct Params {
   PagedBatch s;
-  const uint16_t* Q;
-  const uint16_t* K_pool;
   const float* lse;
   float* mass;
-  long long q_row, k_page;
-  int Hq, Hkv;
-  float scale;
+  float* ws_sum;  // [2 G][256]: pair c's block that began before its range (2 c) or in it (2 c + 1)
+  int* ws_meta;   // [G][kMetaInts]
+  int Hq, Hkv, g_log2, box_log2;
+  float scale_log2;
 };
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct __align__(8) Barriers {
+  uint64_t k_full[2], k_empty[2];
+  uint64_t q_full[kQSlots], q_empty[kQSlots];
+  uint64_t s_full[4], s_empty[4];
+};
+
+// ------------------------------------------------------------------ the list of products
+
+// One sequence's part of the list (of one K/V head).
+struct SeqBlocks {
+  int base, n, len, s_log2;  // s_log2: tokens of a Q tile
+  __host__ __device__ int q_tiles() const { return n > 0 ? ((n - 1) >> s_log2) + 1 : 0; }
+  __host__ __device__ int blocks() const { return n > 0 ? (len + kKeys - 1) / kKeys : 0; }
+  // the first Q tile with a token that sees row 256 k: token 256 k - base, if that is not before 0
+  __host__ __device__ int first_tile(int k) const {
+    const int t = k * kKeys - base;
+    return t <= 0 ? 0 : t >> s_log2;
   }
+  // products of the blocks before k: the first kf blocks take every Q tile, and from there on the first
+  // tile grows by 256 / tokens per block
+  __host__ __device__ long long before(int k) const {
+    const int kf = base < 0 ? 0 : base / kKeys + 1;
+    const long long q = q_tiles();
+    if (k <= kf) return k * q;
+    const long long cb = (base + (1 << s_log2) - 1) >> s_log2;  // ceil(base / tokens)
+    const long long c = k - kf, sum = ((long long)kf + k - 1) * c / 2;
+    return kf * q + c * (q + cb) - (sum << (8 - s_log2));
+  }
+  __host__ __device__ int find(long long w) const {
+    int lo = 0, hi = blocks();
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) <= w) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
+
+struct Start {
+  long long count;
+  int b, h, k, t;
+};
+
+// Walks a pair's pieces: runs of Q tiles against one block.
+struct Walk {
+  const Params& p;
+  long long left;
+  int b, h, k, t0, t1, first, last;  // Q tiles [t0, t1) of the block's [first, last)
+  PagedSeq q;
+  SeqBlocks s;
+  __device__ Walk(const Params& p_, const Start& st) : p(p_) {
+    left = st.count;
+    b = st.b;
+    h = st.h;
+    k = st.k;
+    if (left > 0) {
+      load();
+      cut(st.t);
+    }
+  }
+  __device__ bool done() const { return left <= 0; }
+  __device__ bool whole() const { return t0 == first && t1 == last; }
+  // whether the product after this piece's last one uses the same Q tile
+  __device__ bool same_tile_next() const {
+    return left > t1 - t0 && t1 == last && k + 1 < s.blocks() && s.first_tile(k + 1) == last - 1;
+  }
+  __device__ void next() {
+    left -= t1 - t0;
+    if (left <= 0) return;
+    if (++k == s.blocks()) {
+      k = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.s.B) {  // cannot happen unless the lengths change under the kernel
+            left = 0;
+            return;
+          }
+          load();
+        } while (s.blocks() == 0);
+      }
+    }
+    cut(s.first_tile(k));
+  }
+
+ private:
+  __device__ void load() {
+    q = paged_seq(p.s, b, false);
+    s.base = q.base;
+    s.n = q.n;
+    s.len = q.len;
+    s.s_log2 = 7 - p.g_log2;
+  }
+  __device__ void cut(int t) {
+    t0 = t;
+    first = s.first_tile(k);
+    last = s.q_tiles();
+    const long long e = (long long)t0 + left;
+    t1 = e < last ? (int)e : last;
+  }
+};
+
+// Every thread of the CTA: this pair's share of the list.
+__device__ __forceinline__ void find_start(const Params& p, int worker, int n_workers, Start* out) {
+  __shared__ long long sums[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto seq = [&](int b, bool report) -> SeqBlocks {
+    const PagedSeq q = paged_seq(p.s, b, report);
+    SeqBlocks s;
+    s.base = q.base;
+    s.n = q.n;
+    s.len = q.len;
+    s.s_log2 = 7 - p.g_log2;
+    return s;
+  };
+  auto work_of = [&](int b, bool report) -> long long {
+    if (b >= p.s.B) return 0;
+    const SeqBlocks s = seq(b, report);
+    return s.before(s.blocks()) * p.Hkv;
+  };
+  auto scan = [&](long long x, long long& total) -> long long {  // inclusive prefix over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    __syncthreads();
+    return before + x;
+  };
+  long long mine = 0, all;
+  for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
+  scan(mine, all);
+  const int n = all < n_workers ? (int)all : n_workers;
+  const long long lo = worker < n ? all * worker / n : 0, hi = worker < n ? all * (worker + 1) / n : 0;
+  if (tid == 0) out->count = hi - lo;
+  long long done = 0;
+  for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
+    const long long w = work_of(b0 + tid, false);
+    long long total;
+    const long long upto = done + scan(w, total), from = upto - w;
+    if (from <= lo && lo < upto) {
+      const SeqBlocks s = seq(b0 + tid, false);
+      const long long per_head = w / p.Hkv, r = lo - from;
+      out->b = b0 + tid;
+      out->h = (int)(r / per_head);
+      const long long in = r - out->h * per_head;
+      out->k = s.find(in);
+      out->t = s.first_tile(out->k) + (int)(in - s.before(out->k));
+    }
+    done += total;
+    if (done > lo) break;
+  }
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) mass_kernel(const Params p) {
-  const int b = blockIdx.y, hk = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const PagedSeq q = paged_seq(p.s, b, blockIdx.x == 0 && hk == 0);
-  const int g = p.Hq / p.Hkv, page_mask = (1 << p.s.page_log2) - 1;
-  for (int i = blockIdx.x * 8 + warp; i < q.len; i += gridDim.x * 8) {
-    const int pg = paged_page(p.s, b, i);
-    if (pg < 0) continue;
-    const size_t row = (size_t)(i & page_mask) * p.Hkv + hk;
-    float kf[8];
-    unpack8(reinterpret_cast<const uint4*>(p.K_pool + (size_t)pg * p.k_page + row * kMlaD)[lane], kf);
-    float sum = 0.0f;
-    for (int t = max(0, i - q.base); t < q.n; ++t)
-      for (int h = hk * g; h < hk * g + g; ++h) {
-        float qf[8], x = 0.0f;
-        unpack8(reinterpret_cast<const uint4*>(p.Q + (size_t)(q.q0 + t) * p.q_row + (size_t)h * kMlaD)[lane], qf);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x = fmaf(qf[c], kf[c], x);
-#pragma unroll
-        for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-        sum += expf(x * p.scale - p.lse[(size_t)(q.q0 + t) * p.Hq + h]);
-      }
-    if (lane == 0) atomicAdd(p.mass + (((size_t)pg << p.s.page_log2) * p.Hkv) + row, sum);
-  }
+// ------------------------------------------------------------------ the kernel
+
+__device__ __forceinline__ void group_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mass_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Barriers bar;
+  __shared__ Start start;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) float s_lse[2][kCols];  // by warpgroup: a tile's lse in log2 units
+  __shared__ float s_sum[2][128];                     // by piece: the second warpgroup's sums
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();  // 0: the leader, which issues the MMAs
+  const int worker = (int)blockIdx.x >> 1, n_workers = (int)gridDim.x >> 1;
+  // the tiles need every byte there is, so their 1024-byte alignment is the declaration's
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) raise_device_error(p.s.err, kErrDeviceBounds);
+    return;
+  }
+  uint8_t* sK = smem;
+  uint8_t* sQ = smem + 2 * kKBytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar.k_full[s], 1);
+      mbar_init(&bar.k_empty[s], 1);
+    }
+    for (int s = 0; s < kQSlots; ++s) {
+      mbar_init(&bar.q_full[s], 1);
+      mbar_init(&bar.q_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bar.s_full[s], 1);
+      mbar_init(&bar.s_empty[s], 8);  // a warpgroup's four warps in both CTAs
+    }
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&tmem_base_sh, 512);
+  find_start(p, worker, n_workers, &start);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  const int page_mask = (1 << p.s.page_log2) - 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (all lanes)
+    const int n_tma = 512 >> p.box_log2;  // boxes of 128 K rows: 128 / box rows x 4 chunks, one per lane
+    const int krow = (lane >> 2) << p.box_log2, kchunk = lane & 3;
+    const int g64 = p.g_log2 < 6 ? p.g_log2 : 6;  // heads of a Q box; a group of 128 is two boxes, one per CTA
+    uint32_t piece = 0, u = 0;                    // u: Q tiles loaded
+    bool ok = true, loaded = false;
+    for (Walk w(p, start); !w.done() && ok; w.next(), ++piece) {
+      const uint32_t kb = piece & 1;
+      const int row = w.k * kKeys + 128 * (int)rank + krow;
+      int pg = p.s.n_pages;  // a page that is not there: zeros (outside the tensor map)
+      if (lane < n_tma && row < w.q.len) {
+        pg = paged_page(p.s, w.b, row);
+        if (pg < 0) pg = p.s.n_pages;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&bar.k_empty[kb], ((piece >> 1) & 1) ^ 1, &abort_flag, p.s.err));
+      if (!ok) break;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.k_full[kb], 2 * kKBytes);
+      __syncwarp();
+      if (lane < n_tma)
+        tma_load_4d_pair(sK + kb * kKBytes + kchunk * kKChunk + krow * 128, &map_k, cluster_addr(&bar.k_full[kb], 0),
+                         kchunk * 64, w.h, row & page_mask, pg);
+      for (int t = w.t0; t < w.t1 && ok; ++t) {
+        if (!loaded) {
+          const uint32_t s = u % kQSlots;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&bar.q_empty[s], ((u / kQSlots) & 1) ^ 1, &abort_flag, p.s.err));
+          if (!ok) break;
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.q_full[s], 2 * kQBytes);
+          __syncwarp();
+          if (lane < 4) {
+            const int tok = w.q.q0 + (t << (7 - p.g_log2)) + ((int)rank << (6 - g64));
+            const int head = (w.h << p.g_log2) + (p.g_log2 == 7 ? 64 * (int)rank : 0);
+            tma_load_3d_pair(sQ + s * kQBytes + lane * kQChunk, &map_q, cluster_addr(&bar.q_full[s], 0), lane * 64,
+                             head, p.g_log2 == 7 ? w.q.q0 + t : tok);
+          }
+          ++u;
+        }
+        loaded = t + 1 == w.t1 && w.same_tile_next();  // the next product's Q tile is this one
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(kKeys, kCols, false, false);
+      const uint32_t sKa = smem_u32(sK), sQa = smem_u32(sQ);
+      uint32_t piece = 0, u = 0, n = 0;  // n: products so far (S buffer n & 3)
+      bool ok = true;
+      for (Walk w(p, start); !w.done() && ok; w.next(), ++piece) {
+        const uint32_t kb = piece & 1;
+        ok = mbar_wait(&bar.k_full[kb], (piece >> 1) & 1, &abort_flag, p.s.err);
+        const uint64_t da = smem_desc_sw128(sKa + kb * kKBytes, 16, 1024);
+        for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
+          const uint32_t s = u % kQSlots, sb = n & 3;
+          ok = mbar_wait(&bar.q_full[s], (u / kQSlots) & 1, &abort_flag, p.s.err) &&
+               mbar_wait(&bar.s_empty[sb], ((n >> 2) & 1) ^ 1, &abort_flag, p.s.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t db = smem_desc_sw128(sQa + s * kQBytes, 16, 1024);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
+              mma_ss_pair(tmem + sb * kCols, da + (uint64_t)((c * kKChunk + kk * 32) >> 4),
+                          db + (uint64_t)((c * kQChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
+          mma_commit_pair(&bar.s_full[sb]);
+          const bool last = t + 1 == w.t1;
+          if (!(last && w.same_tile_next())) {
+            mma_commit_pair(&bar.q_empty[s]);
+            ++u;
+          }
+          if (last) mma_commit_pair(&bar.k_empty[kb]);
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ sums (one thread per cache row)
+    const int wg = (warp - 4) >> 2, quarter = warp & 3;
+    const int in_cta = quarter * 32 + lane;  // TMEM lane; also the column whose lse this thread fetches
+    const uint32_t t_lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t n = 0, piece = 0;
+    bool ok = true;
+    int head_flag = 0, tail_flag = 0, tail_b = 0, tail_h = 0, tail_k = 0;  // for ws_meta
+    for (Walk w(p, start); !w.done(); w.next(), ++piece) {
+      const int key = w.k * kKeys + 128 * (int)rank + in_cta;
+      const int n_rows = w.q.n << p.g_log2;  // (token, head) rows of the chunk
+      // column c of tile t: row 128 t + c of the chunk
+      auto lse_of = [&](int t) -> float {
+        const int r = t * kCols + in_cta;
+        if (r >= n_rows) return 0.0f;
+        const size_t tok = w.q.q0 + (r >> p.g_log2);
+        return p.lse[tok * p.Hq + (w.h << p.g_log2) + (r & ((1 << p.g_log2) - 1))] * 1.4426950408889634f;
+      };
+      long long slot = -1;
+      if (wg == 0 && key < w.q.len) {
+        const int pg = paged_page(p.s, w.b, key);
+        if (pg >= 0) slot = (((long long)pg << p.s.page_log2) + (key & page_mask)) * p.Hkv + w.h;
+      }
+      // tokens from here on see this row
+      const long long lo_row = key <= w.q.base ? 0 : (long long)(key - w.q.base) << p.g_log2;
+      float sum = 0.0f, low = 0.0f;  // compensated: sum + low
+      const int mine = (int)((wg - n) & 1);  // this warpgroup's first tile of the piece
+      float next = w.t0 + mine < w.t1 ? lse_of(w.t0 + mine) : 0.0f;
+      for (int t = w.t0 + mine; t < w.t1; t += 2) {
+        const uint32_t at = n + (uint32_t)(t - w.t0), sb = at & 3;
+        float* lse2 = s_lse[wg];
+        group_bar(1 + wg, 128);  // the tile before has been summed
+        lse2[in_cta] = next;
+        if (t + 2 < w.t1) next = lse_of(t + 2);
+        group_bar(1 + wg, 128);
+        ok = mbar_wait(&bar.s_full[sb], (at >> 2) & 1, &abort_flag, p.s.err) && ok;
+        tc_fence_after();
+        const int c_hi = min(kCols, n_rows - t * kCols);                                // uniform
+        const int c_lo = (int)max(0LL, min((long long)kCols, lo_row - (long long)t * kCols));  // this row's
+        const bool all = c_hi == kCols && __all_sync(0xffffffffu, c_lo == 0);
+        float part = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 32 >= c_hi) break;
+          uint32_t s[32];
+          tmem_ld32_nowait(t_lanes + sb * kCols + c * 32, s);
+          tmem_wait_ld_regs(s);
+          float a4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (all) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(lse2 + c * 32 + x);
+              a4[0] += fast_exp2(fmaf(__uint_as_float(s[x]), p.scale_log2, -l.x));
+              a4[1] += fast_exp2(fmaf(__uint_as_float(s[x + 1]), p.scale_log2, -l.y));
+              a4[2] += fast_exp2(fmaf(__uint_as_float(s[x + 2]), p.scale_log2, -l.z));
+              a4[3] += fast_exp2(fmaf(__uint_as_float(s[x + 3]), p.scale_log2, -l.w));
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int col = c * 32 + x;
+              const float e = fast_exp2(fmaf(__uint_as_float(s[x]), p.scale_log2, -lse2[col]));
+              a4[x & 3] += col >= c_lo && col < c_hi ? e : 0.0f;
+            }
+          }
+          part += (a4[0] + a4[1]) + (a4[2] + a4[3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster_tmem(cluster_addr(&bar.s_empty[sb], 0));
+        const float y = part - low, z = sum + y;  // Kahan's sum over the tiles
+        low = (z - sum) - y;
+        sum = z;
+      }
+      n += (uint32_t)(w.t1 - w.t0);
+      // ---- the piece's sum: both warpgroups' tiles
+      if (wg == 1) s_sum[piece & 1][in_cta] = sum;
+      group_bar(3, 256);  // two pieces share a buffer: the first warpgroup has read it before this one's barrier
+      if (wg == 0) {
+        sum += s_sum[piece & 1][in_cta];
+        if (w.whole()) {
+          if (slot >= 0) atomicAdd(p.mass + slot, sum);
+        } else {
+          const int rec = 2 * worker + (w.t0 == w.first ? 1 : 0);
+          p.ws_sum[(size_t)rec * kKeys + 128 * (int)rank + in_cta] = sum;
+        }
+      }
+      if (!w.whole()) {
+        if (w.t0 > w.first) {
+          head_flag = w.t1 == w.last ? 2 : 1;
+        } else {
+          tail_flag = 1;
+          tail_b = w.b;
+          tail_h = w.h;
+          tail_k = w.k;
+        }
+      }
+    }
+    if (rank == 0 && threadIdx.x == 128) {
+      int* m = p.ws_meta + worker * kMetaInts;
+      m[0] = head_flag;
+      m[1] = tail_flag;
+      m[2] = tail_b;
+      m[3] = tail_h;
+      m[4] = tail_k;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Adds up the partial sums of a block that began in pair c's range and went on in pairs c+1, c+2, ...,
+// in that order, one thread per cache row.
+__global__ void __launch_bounds__(kKeys) add_kernel(const Params p, int n_workers) {
+  const int c = blockIdx.x;
+  const int* meta = p.ws_meta + c * kMetaInts;
+  if (!meta[1]) return;
+  const int b = meta[2], h = meta[3], key = meta[4] * kKeys + threadIdx.x;
+  if (key >= paged_len(p.s, b, false)) return;
+  float sum = p.ws_sum[(size_t)(2 * c + 1) * kKeys + threadIdx.x];
+  for (int k = c + 1; k < n_workers; ++k) {
+    const int flag = p.ws_meta[k * kMetaInts];
+    if (!flag) break;
+    sum += p.ws_sum[(size_t)(2 * k) * kKeys + threadIdx.x];
+    if (flag == 2) break;
+  }
+  const int pg = paged_page(p.s, b, key);
+  if (pg < 0) return;
+  const int in = key & ((1 << p.s.page_log2) - 1);
+  atomicAdd(p.mass + (((size_t)pg << p.s.page_log2) + in) * p.Hkv + h, sum);
+}
+
+// Pairs of a launch: one per two SMs of the current device.
+int pairs_of_device() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!cache[dev]) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2 ||
+        cudaFuncSetAttribute(mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) {
+      launch_status();
+      return 0;
+    }
+    cache[dev] = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+  }
+  return cache[dev];
+}
+
+size_t workspace_bytes_of(int pairs) { return (size_t)pairs * (2 * kKeys * 4 + kMetaInts * 4); }
 
 }  // namespace
 }  // namespace hcadsa
 
 extern "C" size_t mla_paged_attn_mass_workspace_size(int B, int T, int Hq, int Hkv) {
-  (void)B;
-  (void)T;
-  (void)Hq;
-  (void)Hkv;
-  return 0;
+  using namespace hcadsa;
+  if (B <= 0 || T <= 0 || Hkv <= 0 || check_query_sizes(T, Hq, Hkv, kMlaD, 1.0f) != HCADSA_OK) return 0;
+  return workspace_bytes_of(pairs_of_device());
 }
 
 extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,
@@ -84,18 +519,37 @@ extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_r
       !aligned4(lse) || !aligned4(mass))
     return HCADSA_ERR_ALIGN;
   if (B == 0 || T == 0) return HCADSA_OK;
+  const int pairs = pairs_of_device();
+  if (pairs <= 0) return HCADSA_ERR_CUDA;
+  if (!workspace || workspace_bytes < workspace_bytes_of(pairs)) return HCADSA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return HCADSA_ERR_ALIGN;
   Params p;
   p.s = paged_batch(table, cu_q, kv_len, B, T, n_pages, page, max_pages);
-  p.Q = Q;
-  p.K_pool = K_pool;
   p.lse = lse;
   p.mass = mass;
-  p.q_row = q_row_stride;
-  p.k_page = k_page_stride;
+  p.ws_sum = static_cast<float*>(workspace);
+  p.ws_meta = reinterpret_cast<int*>(p.ws_sum + (size_t)2 * pairs * kKeys);
   p.Hq = Hq;
   p.Hkv = Hkv;
-  p.scale = scale;
-  const long long cap = (long long)max_pages * page;
-  mass_kernel<<<dim3((unsigned)(cap / 8 < 4096 ? cap / 8 : 4096), B, Hkv), 256, 0, as_stream(stream)>>>(p);
+  p.g_log2 = log2_of(Hq / Hkv);
+  p.box_log2 = page < 64 ? log2_of(page) : 6;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  CUtensorMap mq, mk;
+  {
+    const int g = p.g_log2 < 6 ? 1 << p.g_log2 : 64;
+    const uint64_t dims[3] = {(uint64_t)kMlaD, (uint64_t)Hq, (uint64_t)T};
+    const uint64_t strides[2] = {(uint64_t)kMlaD * 2, (uint64_t)q_row_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)g, (uint32_t)(64 / g)};
+    if (!encode_tmap_bf16(&mq, 3, const_cast<hcadsa_bf16*>(Q), dims, strides, box, true)) return HCADSA_ERR_CUDA;
+  }
+  {
+    const uint64_t dims[4] = {(uint64_t)kMlaD, (uint64_t)Hkv, (uint64_t)page, (uint64_t)n_pages};
+    const uint64_t strides[3] = {(uint64_t)kMlaD * 2, (uint64_t)Hkv * kMlaD * 2, (uint64_t)k_page_stride * 2};
+    const uint32_t box[4] = {64, 1, 1u << p.box_log2, 1};
+    if (!encode_tmap_bf16(&mk, 4, const_cast<hcadsa_bf16*>(K_pool), dims, strides, box, true)) return HCADSA_ERR_CUDA;
+  }
+  mass_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, p);
+  HCADSA_TRY(launch_status());
+  add_kernel<<<pairs, kKeys, 0, as_stream(stream)>>>(p, pairs);
   return launch_status();
 }
