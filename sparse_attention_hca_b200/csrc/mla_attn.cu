@@ -237,7 +237,7 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   if (tid == 0) out->count = hi - lo;
   long long done = 0;
   for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
-    const long long w = work_of(b0 + tid, false);
+    const long long w = p.s.B <= kThreads ? mine : work_of(b0 + tid, false);
     long long total;
     const long long upto = done + scan(w, total), from = upto - w;
     if (from <= lo && lo < upto) {
