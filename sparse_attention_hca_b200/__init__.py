@@ -22,7 +22,9 @@ Functions (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -51,6 +53,8 @@ class HcaDsaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -540,53 +544,89 @@ def hca_attn_bwd(Q, Kc, Vc, Kw, Vw, O, dO, lse, *, win_start: int = 0, q_offset:
 
 
 def _need_pool(t, name, like=None):
-    """A pool [n_pages, page, Hkv, d] bf16: dense within a page, any page stride that keeps them apart."""
-    if t.dtype != torch.bfloat16:
+    """A pool [n_pages, page, Hkv, d] bf16: dense within a page, any page stride that keeps them apart.
+    Returns its sizes and its page stride in elements."""
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 4 or (like is not None and t.shape != like.shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"{'[n_pages, page, Hkv, d]' if like is None else tuple(like.shape)}")
-    n_pages, page, Hkv, d = t.shape
-    st = t.stride()
-    if st[3] != 1 or (Hkv > 1 and st[2] != d) or (page > 1 and st[1] != Hkv * d) or (n_pages > 1 and
-                                                                                    st[0] < page * Hkv * d):
-        raise ValueError(f"{name} must be contiguous within a page, with pages apart (strides {st})")
-    return n_pages, page, Hkv, d, (st[0] if n_pages > 1 else page * Hkv * d)
+    shape = t.shape
+    if len(shape) != 4 or (like is not None and shape != like):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
+                         f"{'[n_pages, page, Hkv, d]' if like is None else tuple(like)}")
+    n_pages, page, Hkv, d = shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 or (Hkv > 1 and s2 != d) or (page > 1 and s1 != Hkv * d) or (n_pages > 1 and s0 < page * Hkv * d):
+        raise ValueError(f"{name} must be contiguous within a page, with pages apart (strides {t.stride()})")
+    return n_pages, page, Hkv, d, (s0 if n_pages > 1 else page * Hkv * d)
 
 
 def _need_rows(t, name, H=None):
-    """Packed rows [T, H, d] bf16: dense within a row, any row stride that keeps them apart."""
-    if t.dtype != torch.bfloat16:
+    """Packed rows [T, H, d] bf16: dense within a row, any row stride that keeps them apart.  Returns
+    the sizes and the row stride in elements."""
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (H is not None and t.shape[1] != H):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [T, {'H' if H is None else H}, d]")
-    T, h, d = t.shape
-    st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != d) or (T > 1 and st[0] < h * d):
-        raise ValueError(f"{name} must be contiguous within a row, with rows apart (strides {st})")
-    return T, h, d, (st[0] if T > 1 else h * d)
+    shape = t.shape
+    if len(shape) != 3 or (H is not None and shape[1] != H):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [T, {'H' if H is None else H}, d]")
+    T, h, d = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != d) or (T > 1 and s0 < h * d):
+        raise ValueError(f"{name} must be contiguous within a row, with rows apart (strides {t.stride()})")
+    return T, h, d, (s0 if T > 1 else h * d)
+
+
+def _need_exact(t, dtype, name, shape):
+    """_need with an exact shape, without its cost where everything fits."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, dtype, name, shape)
 
 
 def _need_batch(table, kv_len, cu_q=None, seen=None):
-    _need(table, torch.int32, "table")
     if table.dim() != 2:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
     B, max_pages = table.shape
-    _need(kv_len, torch.int32, "kv_len", (B,))
+    _need_exact(table, torch.int32, "table", (B, max_pages))
+    _need_exact(kv_len, torch.int32, "kv_len", (B,))
     if cu_q is not None:
-        _need(cu_q, torch.int32, "cu_q", (B + 1,))
+        _need_exact(cu_q, torch.int32, "cu_q", (B + 1,))
     if seen is not None:
-        _need(seen, torch.int32, "seen", (B,))
+        _need_exact(seen, torch.int32, "seen", (B,))
     return B, max_pages
 
 
-def _alloc(stream, make):
-    """Device memory for a call on `stream`: taken from that stream's pool, so that the allocator
-    does not hand it out again before the call has run."""
+def _device_and_stream(stream, *tensors):
+    """The current device, on which every tensor has to lie, and the raw stream of the call."""
+    first = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != first:
+            _on_device(*tensors)
+            raise ValueError("the tensors lie on different devices")
+    if first < 0 or first != torch._C._cuda_getDevice():
+        _on_device(*tensors)
+    return first, (torch._C._cuda_getCurrentRawStream(first) if stream is None else stream.cuda_stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(call, device, B, T, Hq, Hkv):
+    return getattr(lib(), call)(B, T, Hq, Hkv)  # on `device`, the current one
+
+
+def _empty(shape, dtype, device, stream):
+    """Device memory for a call on `stream`: taken from that stream's pool, so that the allocator does not hand it
+    out again before the call has run."""
     if stream is None:
-        return make()
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return make()
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(call, workspace, device, dev_index, stream, B, T, Hq, Hkv):
+    """(workspace, its bytes) of an attention call: the caller's, or one from the allocator."""
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return workspace, workspace.numel() * workspace.element_size()
+    n = _workspace_bytes(call, dev_index, B, T, Hq, Hkv)
+    return (_empty(n, torch.uint8, device, stream) if n else None), n
 
 
 def _addr(t):
@@ -599,20 +639,20 @@ def mla_cache_append(K, V, K_pool, V_pool, table, cu_q, kv_len, *, seen=None, po
     the new rows).  pos (int32) and mass (fp32) [n_pages, page, Hkv], where given: pos = seen - n_b + i (seen: [B]
     int32, tokens so far; kv_len if None), mass = 0.  Returns (K_pool, V_pool)."""
     n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
+    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
     T, _, dk, k_row = _need_rows(K, "K", Hkv)
     Tv, _, dv, v_row = _need_rows(V, "V", Hkv)
     if Tv != T or dk != d or dv != d:
         raise ValueError(f"K and V have shapes {tuple(K.shape)} and {tuple(V.shape)}, expected [T, {Hkv}, {d}] of one T")
     B, max_pages = _need_batch(table, kv_len, cu_q, seen)
     if pos is not None:
-        _need(pos, torch.int32, "pos", (n_pages, page, Hkv))
+        _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
     if mass is not None:
-        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
-    _on_device(K, V, K_pool, V_pool, table, cu_q, kv_len, seen, pos, mass)
-    st = lib().mla_cache_append(K.data_ptr(), V.data_ptr(), k_row, v_row, K_pool.data_ptr(), V_pool.data_ptr(),
-                                k_page, v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _addr(seen), _addr(pos), _addr(mass), B, T, n_pages, page,
-                                max_pages, Hkv, d, _stream(stream))
+        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _, raw = _device_and_stream(stream, K, V, K_pool, V_pool, table, cu_q, kv_len, seen, pos, mass)
+    st = lib().mla_cache_append(K.data_ptr(), V.data_ptr(), k_row, v_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page,
+                                v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _addr(seen), _addr(pos),
+                                _addr(mass), B, T, n_pages, page, max_pages, Hkv, d, raw)
     _check(st, "mla_cache_append")
     return K_pool, V_pool
 
@@ -623,35 +663,26 @@ def mla_paged_attn_fwd(Q, K_pool, V_pool, table, cu_q, kv_len, *, scale: float |
     the kv_len[b] rows of its pages; new token i sees the rows <= kv_len[b] - n_b + i.  Pools, table and lengths as
     for mla_cache_append.  Rows of O and lse behind cu_q[B] are left as they are."""
     n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
+    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
     T, Hq, dq, q_row = _need_rows(Q, "Q")
     if dq != d:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
     B, max_pages = _need_batch(table, kv_len, cu_q)
     if O is not None:
-        _need(O, torch.bfloat16, "O", (T, Hq, d))
+        _need_exact(O, torch.bfloat16, "O", (T, Hq, d))
     if lse is not None:
-        _need(lse, torch.float32, "lse", (T, Hq))
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on_device(Q, K_pool, V_pool, table, cu_q, kv_len, O, lse, workspace)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    dev = Q.device
+        _need_exact(lse, torch.float32, "lse", (T, Hq))
+    dev, raw = _device_and_stream(stream, Q, K_pool, V_pool, table, cu_q, kv_len, O, lse, workspace)
+    device = Q.device
     if O is None:
-        O = _alloc(stream, lambda: torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev))
+        O = _empty((T, Hq, d), torch.bfloat16, device, stream)
     if return_lse and lse is None:
-        lse = _alloc(stream, lambda: torch.empty((T, Hq), dtype=torch.float32, device=dev))
-    L = lib()
-    if workspace is None:
-        ws_bytes = L.mla_paged_attn_fwd_workspace_size(B, T, Hq, Hkv)
-        if ws_bytes:
-            workspace = _alloc(stream, lambda: torch.empty(ws_bytes, dtype=torch.uint8, device=dev))
-    else:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    st = L.mla_paged_attn_fwd(Q.data_ptr(), q_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), O.data_ptr(),
-                              _addr(lse), B, T, n_pages, page, max_pages, Hq, Hkv, d, scale, _addr(workspace),
-                              ws_bytes, _stream(stream))
+        lse = _empty((T, Hq), torch.float32, device, stream)
+    workspace, ws_bytes = _scratch("mla_paged_attn_fwd_workspace_size", workspace, device, dev, stream, B, T, Hq, Hkv)
+    st = lib().mla_paged_attn_fwd(Q.data_ptr(), q_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page,
+                                  table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), O.data_ptr(), _addr(lse), B, T,
+                                  n_pages, page, max_pages, Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
+                                  _addr(workspace), ws_bytes, raw)
     _check(st, "mla_paged_attn_fwd")
     return (O, lse) if return_lse else O
 
@@ -666,27 +697,19 @@ def mla_paged_attn_mass(Q, K_pool, table, cu_q, kv_len, lse, *, scale: float | N
     if dq != d:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
     B, max_pages = _need_batch(table, kv_len, cu_q)
-    _need(lse, torch.float32, "lse", (T, Hq))
+    _need_exact(lse, torch.float32, "lse", (T, Hq))
     if mass is not None:
-        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on_device(Q, K_pool, table, cu_q, kv_len, lse, mass, workspace)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    dev = Q.device
+        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    dev, raw = _device_and_stream(stream, Q, K_pool, table, cu_q, kv_len, lse, mass, workspace)
+    device = Q.device
     if mass is None:
-        mass = _alloc(stream, lambda: torch.zeros((n_pages, page, Hkv), dtype=torch.float32, device=dev))
-    L = lib()
-    if workspace is None:
-        ws_bytes = L.mla_paged_attn_mass_workspace_size(B, T, Hq, Hkv)
-        if ws_bytes:
-            workspace = _alloc(stream, lambda: torch.empty(ws_bytes, dtype=torch.uint8, device=dev))
-    else:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    st = L.mla_paged_attn_mass(Q.data_ptr(), q_row, K_pool.data_ptr(), k_page, table.data_ptr(),
-                               cu_q.data_ptr(), kv_len.data_ptr(), lse.data_ptr(), mass.data_ptr(), B, T, n_pages,
-                               page, max_pages, Hq, Hkv, d, scale, _addr(workspace), ws_bytes, _stream(stream))
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            mass = torch.zeros((n_pages, page, Hkv), dtype=torch.float32, device=device)
+    workspace, ws_bytes = _scratch("mla_paged_attn_mass_workspace_size", workspace, device, dev, stream, B, T, Hq, Hkv)
+    st = lib().mla_paged_attn_mass(Q.data_ptr(), q_row, K_pool.data_ptr(), k_page, table.data_ptr(), cu_q.data_ptr(),
+                                   kv_len.data_ptr(), lse.data_ptr(), mass.data_ptr(), B, T, n_pages, page, max_pages,
+                                   Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, _addr(workspace),
+                                   ws_bytes, raw)
     _check(st, "mla_paged_attn_mass")
     return mass
 
@@ -698,28 +721,27 @@ def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int
     [B] int32 (seen None: kv_len) -> moves [B, Hkv, n, 2] int32, entry i = (i-th staying row >= budget, i-th freed row <
     budget), (-1, -1) past the last, n = min(budget, max_pages * page - budget); new_len [B] int32.  Writes nothing else:
     mla_cache_move makes the moves."""
-    _need(mass, torch.float32, "mass")
     if mass.dim() != 3:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected [n_pages, page, Hkv]")
     n_pages, page, Hkv = mass.shape
-    _need(pos, torch.int32, "pos", mass.shape)
+    _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
     B, max_pages = _need_batch(table, kv_len, seen=seen)
     n = max(0, min(budget, max_pages * page - budget))
     if moves is not None:
-        _need(moves, torch.int32, "moves", (B, Hkv, n, 2))
+        _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
     if new_len is not None:
-        _need(new_len, torch.int32, "new_len", (B,))
+        _need_exact(new_len, torch.int32, "new_len", (B,))
         if new_len.data_ptr() == kv_len.data_ptr():
             raise ValueError("new_len must not be kv_len: kv_len is read while new_len is written")
-    _on_device(mass, pos, table, kv_len, seen, moves, new_len)
-    dev = mass.device
+    _, raw = _device_and_stream(stream, mass, pos, table, kv_len, seen, moves, new_len)
     if moves is None:
-        moves = _alloc(stream, lambda: torch.empty((B, Hkv, n, 2), dtype=torch.int32, device=dev))
+        moves = _empty((B, Hkv, n, 2), torch.int32, mass.device, stream)
     if new_len is None:
-        new_len = _alloc(stream, lambda: torch.empty(B, dtype=torch.int32, device=dev))
+        new_len = _empty((B,), torch.int32, mass.device, stream)
     st = lib().mla_evict_select(mass.data_ptr(), pos.data_ptr(), table.data_ptr(), kv_len.data_ptr(), _addr(seen),
                                 moves.data_ptr(), new_len.data_ptr(), B, n_pages, page, max_pages, Hkv, budget, n_sink,
-                                n_recent, n, _stream(stream))
+                                n_recent, n, raw)
     _check(st, "mla_evict_select")
     return moves, new_len
 
@@ -729,21 +751,21 @@ def mla_cache_move(moves, K_pool, V_pool, table, *, pos=None, mass=None, stream=
     of sequence b and that K/V head (K, V, and pos and mass where given) goes to row `to`.  No row may be written twice,
     or written by one entry and read by another.  Returns (K_pool, V_pool)."""
     n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool)[4]
-    _need(table, torch.int32, "table")
+    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
     if table.dim() != 2:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
     B, max_pages = table.shape
-    _need(moves, torch.int32, "moves")
-    if moves.dim() != 4 or moves.shape[0] != B or moves.shape[1] != Hkv or moves.shape[3] != 2:
+    _need_exact(table, torch.int32, "table", (B, max_pages))
+    if moves.dim() != 4:
         raise ValueError(f"moves has shape {tuple(moves.shape)}, expected [{B}, {Hkv}, n, 2]")
+    n = moves.shape[2]
+    _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
     if pos is not None:
-        _need(pos, torch.int32, "pos", (n_pages, page, Hkv))
+        _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
     if mass is not None:
-        _need(mass, torch.float32, "mass", (n_pages, page, Hkv))
-    _on_device(moves, table, K_pool, V_pool, pos, mass)
-    st = lib().mla_cache_move(moves.data_ptr(), table.data_ptr(), K_pool.data_ptr(), V_pool.data_ptr(),
-                              k_page, v_page, _addr(pos), _addr(mass), B, moves.shape[2], n_pages,
-                              page, max_pages, Hkv, d, _stream(stream))
+        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _, raw = _device_and_stream(stream, moves, table, K_pool, V_pool, pos, mass)
+    st = lib().mla_cache_move(moves.data_ptr(), table.data_ptr(), K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page,
+                              _addr(pos), _addr(mass), B, n, n_pages, page, max_pages, Hkv, d, raw)
     _check(st, "mla_cache_move")
     return K_pool, V_pool

@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_tok = row >> p.g_log2, my_head = row & ((1 << p.g_log2) - 1);
     const uint32_t t_lanes = tmem + (static_cast<uint32_t>(lane0) << 16);
     const int tid = threadIdx.x - 128;
+    const uint32_t ready0 = cluster_addr(&bar.p_ready[0], 0);
     uint32_t g = 0, u = 0, tails = 0;
     bool ok = true;
     int head_flag = 0, tail_flag = 0, tail_tok = 0, tail_n = 0, tail_h = 0;  // for ws_meta
@@ -596,9 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if constexpr (kPair) {
-            const uint32_t ready = cluster_addr(&bar.p_ready[g & 1], 0);
-            if (tail) arrive_cluster(ready);
-            else arrive_cluster_tmem(ready);
+            const uint32_t ready = ready0 + (g & 1) * 8;
+            if (tail) arrive_cluster(ready);  // shared memory was written
+            else arrive_cluster_relaxed(ready);
           } else {
             mbar_arrive(&bar.p_ready[g & 1]);
           }

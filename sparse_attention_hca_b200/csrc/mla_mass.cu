@@ -219,46 +219,6 @@ __device__ __forceinline__ void group_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-// acc += (2^x.x, 2^x.y) without the SFU: 2^x = 2^n 2^f, n the nearest integer, f in [-1/2, 1/2], 2^f by
-// a polynomial of degree 5 fitted to the least relative error (1.6e-7 with these fp32 coefficients).
-// Adding 1.5 * 2^23 + 127 leaves n + 127, the exponent field of 2^n, in the low bits of the sum.  Below
-// 2^-126 the result stays there; NaN stays NaN; x has to be below 127.
-__device__ __forceinline__ float2 add_exp2_fma(float2 acc, float2 x) {
-  float2 f;
-  asm("max.NaN.f32 %0, %2, 0fC2FC0000;\n\tmax.NaN.f32 %1, %3, 0fC2FC0000;" : "=f"(f.x), "=f"(f.y) : "f"(x.x), "f"(x.y));
-  const float magic = 12583039.0f;
-  const float2 t = add2(f, make_float2(magic, magic));
-  f = add2(f, add2(make_float2(magic, magic), make_float2(-t.x, -t.y)));
-  auto both = [](float c) { return make_float2(c, c); };
-  float2 y = fma2(both(0.001327647129073739f), f, both(0.009675541892647743f));
-  y = fma2(y, f, both(0.05550713092088699f));
-  y = fma2(y, f, both(0.24022120237350464f));
-  y = fma2(y, f, both(0.6931469440460205f));
-  y = fma2(y, f, both(1.0000001192092896f));
-  const float2 p2 = make_float2(__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23));
-  return fma2(y, p2, acc);
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mass_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ Params p) {
@@ -387,10 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int in_cta = quarter * 32 + lane;  // TMEM lane; also the column whose lse this thread fetches
     const uint32_t t_lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     const int group_mask = (1 << p.g_log2) - 1;
     const size_t lse_step = (size_t)((kGroups * kCols) >> p.g_log2) * p.Hq;  // to this group's next tile
     float* col = s_col[wg];
+    const uint32_t empty_addr = cluster_addr(&bar.s_empty[wg], 0);
     uint32_t n = 0, shared_pieces = 0;
     bool ok = true, handed = false;  // handed: s_col holds sums that the finishing group has not read yet
     int head_flag = 0, tail_flag = 0, tail_b = 0, tail_h = 0, tail_k = 0;  // for ws_meta
@@ -401,19 +361,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int r = (w.t0 + mine) * kCols + in_cta;  // the row whose lse this thread fetches next
       const float* lse_at = p.lse + (size_t)(w.q.q0 + (r >> p.g_log2)) * p.Hq + (w.h << p.g_log2) + (r & group_mask);
       auto fetch = [&]() -> float {
-        const float v = r < n_rows ? *lse_at * -1.4426950408889634f : 0.0f;
+        const float v = r < n_rows ? *lse_at : 0.0f;  // scaled when it is used, so that nothing waits here
         r += kGroups * kCols;
         lse_at += lse_step;
         return v;
       };
-      long long slot = -1;
       // the warpgroup of the piece's last tile finishes the piece
       const int tiles = w.t1 - w.t0, finisher = (int)((n + (uint32_t)tiles - 1) & (kGroups - 1));
       const bool finish = finisher == wg;
-      if (finish && key < w.q.len) {
-        const int pg = paged_page(p.s, w.b, key);
-        if (pg >= 0) slot = (((long long)pg << p.s.page_log2) + (key & page_mask)) * p.Hkv + w.h;
-      }
+      // this row's page, looked up now and looked at when the piece is done
+      const bool mine_to_add = finish && key < w.q.len;
+      int pg = 0;
+      if (mine_to_add) pg = p.s.table[(size_t)w.b * p.s.max_pages + (key >> p.s.page_log2)];
       // tokens from here on see this row
       const int lo_row = min(max(key - w.q.base, 0), w.q.n) << p.g_log2;
       float sum = 0.0f, low = 0.0f;  // compensated: sum + low
@@ -426,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t at = n + (uint32_t)(t - w.t0), sb = (uint32_t)wg;
         wait_free();
         group_bar(1 + wg, 128);  // the tile before has been summed
-        col[in_cta] = next;
+        col[in_cta] = next * -1.4426950408889634f;
         if (t + kGroups < w.t1) next = fetch();
         group_bar(1 + wg, 128);
         ok = mbar_wait(&bar.s_full[sb], (at >> 2) & 1, &abort_flag, p.s.err) && ok;
@@ -434,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int c_hi = min(kCols, n_rows - t * kCols);                                // uniform
         const int c_lo = max(0, min(kCols, lo_row - t * kCols));                              // this row's
         const bool all = c_hi == kCols && __all_sync(0xffffffffu, c_lo == 0);
-        float2 a2[3] = {};
+        float a4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c * 32 >= c_hi) break;
@@ -445,29 +404,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
               const float4 l = *reinterpret_cast<const float4*>(col + c * 32 + x);
-              const float2 u0 = fma2(make_float2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), scale2,
-                                     make_float2(l.x, l.y));
-              const float2 u1 = fma2(make_float2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), scale2,
-                                     make_float2(l.z, l.w));
-              a2[0] = add2(a2[0], make_float2(fast_exp2(u0.x), fast_exp2(u0.y)));
-              // three of sixteen pairs on the FMA units, where they cost 14 issue slots each
-              if (x == 0 || x == 12 || x == 24) a2[1] = add_exp2_fma(a2[1], u1);
-              else a2[2] = add2(a2[2], make_float2(fast_exp2(u1.x), fast_exp2(u1.y)));
+              a4[0] += fast_exp2(fmaf(__uint_as_float(v[x]), p.scale_log2, l.x));
+              a4[1] += fast_exp2(fmaf(__uint_as_float(v[x + 1]), p.scale_log2, l.y));
+              a4[2] += fast_exp2(fmaf(__uint_as_float(v[x + 2]), p.scale_log2, l.z));
+              a4[3] += fast_exp2(fmaf(__uint_as_float(v[x + 3]), p.scale_log2, l.w));
             }
           } else {
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
               const int cc = c * 32 + x;
               const float e = fast_exp2(fmaf(__uint_as_float(v[x]), p.scale_log2, col[cc]));
-              a2[x % 3].x += cc >= c_lo && cc < c_hi ? e : 0.0f;
+              a4[x & 3] += cc >= c_lo && cc < c_hi ? e : 0.0f;
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster_tmem(cluster_addr(&bar.s_empty[sb], 0));
-        const float2 b2 = add2(add2(a2[0], a2[1]), a2[2]);
-        const float y = (b2.x + b2.y) - low, z = sum + y;  // Kahan's sum over the tiles
+        if (lane == 0) arrive_cluster_relaxed(empty_addr);
+        const float y = ((a4[0] + a4[1]) + (a4[2] + a4[3])) - low, z = sum + y;  // Kahan's sum over the tiles
         low = (z - sum) - y;
         sum = z;
       }
@@ -495,7 +449,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       n += (uint32_t)tiles;
       if (finish) {
         if (w.whole()) {
-          if (slot >= 0) atomicAdd(p.mass + slot, sum);
+          if (mine_to_add) {
+            if (pg >= 0 && pg < p.s.n_pages)
+              atomicAdd(p.mass + (((size_t)pg << p.s.page_log2) + (key & page_mask)) * p.Hkv + w.h, sum);
+            else
+              raise_device_error(p.s.err, kErrDeviceBounds);
+          }
         } else {
           const int rec = 2 * worker + (w.t0 == w.first ? 1 : 0);
           p.ws_sum[(size_t)rec * kKeys + 128 * (int)rank + in_cta] = sum;

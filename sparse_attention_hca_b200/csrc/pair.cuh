@@ -25,10 +25,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// The same with release at CTA scope only: for hand-overs whose data are TMEM accumulators (ordered
-// by tcgen05.fence::before_thread_sync), where the cluster-scope release would be a needless flush.
-__device__ __forceinline__ void arrive_cluster_tmem(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// The same without release semantics, for hand-overs of TMEM accumulators, which
+// tcgen05.fence::before_thread_sync orders: a release would first wait for the thread's other memory
+// operations (at cluster scope about 1000 cycles in the attention kernel, per tile).
+__device__ __forceinline__ void arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
