@@ -610,23 +610,23 @@ def _workspace_bytes(call, device, B, T, Hq, Hkv):
     return getattr(lib(), call)(B, T, Hq, Hkv)  # on `device`, the current one
 
 
-def _empty(shape, dtype, device, stream):
-    """Device memory for a call on `stream`: taken from that stream's pool, so that the allocator does not hand it
-    out again before the call has run."""
+def _empty(like, shape, dtype, stream):
+    """Device memory (on `like`'s device) for a call on `stream`: taken from that stream's pool, so that the allocator
+    does not hand it out again before the call has run."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(call, workspace, device, dev_index, stream, B, T, Hq, Hkv):
+def _scratch(call, workspace, like, device, stream, B, T, Hq, Hkv):
     """(workspace, its bytes) of an attention call: the caller's, or one from the allocator."""
     if workspace is not None:
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         return workspace, workspace.numel() * workspace.element_size()
-    n = _workspace_bytes(call, dev_index, B, T, Hq, Hkv)
-    return (_empty(n, torch.uint8, device, stream) if n else None), n
+    n = _workspace_bytes(call, device, B, T, Hq, Hkv)
+    return (_empty(like, n, torch.uint8, stream) if n else None), n
 
 
 def _addr(t):
@@ -673,12 +673,11 @@ def mla_paged_attn_fwd(Q, K_pool, V_pool, table, cu_q, kv_len, *, scale: float |
     if lse is not None:
         _need_exact(lse, torch.float32, "lse", (T, Hq))
     dev, raw = _device_and_stream(stream, Q, K_pool, V_pool, table, cu_q, kv_len, O, lse, workspace)
-    device = Q.device
     if O is None:
-        O = _empty((T, Hq, d), torch.bfloat16, device, stream)
+        O = _empty(Q, (T, Hq, d), torch.bfloat16, stream)
     if return_lse and lse is None:
-        lse = _empty((T, Hq), torch.float32, device, stream)
-    workspace, ws_bytes = _scratch("mla_paged_attn_fwd_workspace_size", workspace, device, dev, stream, B, T, Hq, Hkv)
+        lse = _empty(Q, (T, Hq), torch.float32, stream)
+    workspace, ws_bytes = _scratch("mla_paged_attn_fwd_workspace_size", workspace, Q, dev, stream, B, T, Hq, Hkv)
     st = lib().mla_paged_attn_fwd(Q.data_ptr(), q_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page,
                                   table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), O.data_ptr(), _addr(lse), B, T,
                                   n_pages, page, max_pages, Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale,
@@ -701,11 +700,10 @@ def mla_paged_attn_mass(Q, K_pool, table, cu_q, kv_len, lse, *, scale: float | N
     if mass is not None:
         _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
     dev, raw = _device_and_stream(stream, Q, K_pool, table, cu_q, kv_len, lse, mass, workspace)
-    device = Q.device
     if mass is None:
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-            mass = torch.zeros((n_pages, page, Hkv), dtype=torch.float32, device=device)
-    workspace, ws_bytes = _scratch("mla_paged_attn_mass_workspace_size", workspace, device, dev, stream, B, T, Hq, Hkv)
+            mass = Q.new_zeros((n_pages, page, Hkv), dtype=torch.float32)
+    workspace, ws_bytes = _scratch("mla_paged_attn_mass_workspace_size", workspace, Q, dev, stream, B, T, Hq, Hkv)
     st = lib().mla_paged_attn_mass(Q.data_ptr(), q_row, K_pool.data_ptr(), k_page, table.data_ptr(), cu_q.data_ptr(),
                                    kv_len.data_ptr(), lse.data_ptr(), mass.data_ptr(), B, T, n_pages, page, max_pages,
                                    Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, _addr(workspace),
@@ -736,9 +734,9 @@ def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int
             raise ValueError("new_len must not be kv_len: kv_len is read while new_len is written")
     _, raw = _device_and_stream(stream, mass, pos, table, kv_len, seen, moves, new_len)
     if moves is None:
-        moves = _empty((B, Hkv, n, 2), torch.int32, mass.device, stream)
+        moves = _empty(mass, (B, Hkv, n, 2), torch.int32, stream)
     if new_len is None:
-        new_len = _empty((B,), torch.int32, mass.device, stream)
+        new_len = _empty(mass, (B,), torch.int32, stream)
     st = lib().mla_evict_select(mass.data_ptr(), pos.data_ptr(), table.data_ptr(), kv_len.data_ptr(), _addr(seen),
                                 moves.data_ptr(), new_len.data_ptr(), B, n_pages, page, max_pages, Hkv, budget, n_sink,
                                 n_recent, n, raw)

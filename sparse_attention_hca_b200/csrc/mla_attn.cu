@@ -304,6 +304,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (threadIdx.x == 32 * 2) {
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
   if (warp == 1) {
     if constexpr (kPair) {
       tmem_alloc_pair(&tmem_base_sh, 512);
@@ -671,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  launch_dependents();
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
@@ -691,6 +697,7 @@ constexpr int kCombineWarps = 8;
 constexpr int kMaxWorkers = 160;
 
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p, int n_workers, int n_rows) {
+  wait_for_primary();
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
   const int* meta = p.ws_meta + c * kMetaInts;
@@ -808,9 +815,8 @@ hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
-  combine_kernel<<<dim3(workers, Shape<kPair>::kRows / kCombineWarps), 32 * kCombineWarps, 0, stream>>>(
-      p, workers, Shape<kPair>::kRows);
-  return launch_status();
+  return launch_after(combine_kernel, dim3(workers, Shape<kPair>::kRows / kCombineWarps), 32 * kCombineWarps, stream,
+                      p, workers, (int)Shape<kPair>::kRows);
 }
 
 }  // namespace

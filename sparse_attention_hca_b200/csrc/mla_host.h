@@ -61,6 +61,23 @@ inline PagedBatch paged_batch(const int32_t* table, const int32_t* cu_q, const i
   return s;
 }
 
+// Launches a kernel that follows one on the same stream and calls wait_for_primary() before it reads
+// what that one wrote: its launch overlaps the end of the first.
+template <typename... Params, typename... Args>
+hcadsa_status launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, Params(args)...) != cudaSuccess) return launch_status();
+  return launch_status();
+}
+
 #define HCADSA_TRY(expr)                             \
   do {                                               \
     const hcadsa_status try_st_ = (expr);            \

@@ -257,6 +257,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (threadIdx.x == 32 * 2) {
+    tma_prefetch_desc(&map_q);
+    tma_prefetch_desc(&map_k);
+  }
   if (warp == 1) tmem_alloc_pair(&tmem_base_sh, 512);
   find_start(p, worker, n_workers, &start);
   tc_fence_before();
@@ -481,6 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   }
 
+  launch_dependents();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no MMA of the pair and no cross-CTA arrival is pending any more
@@ -491,6 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Adds up the partial sums of a block that began in pair c's range and went on in pairs c+1, c+2, ...,
 // in that order, one thread per cache row.
 __global__ void __launch_bounds__(kKeys) add_kernel(const Params p, int n_workers) {
+  wait_for_primary();
   const int c = blockIdx.x;
   const int* meta = p.ws_meta + c * kMetaInts;
   if (!meta[1]) return;
@@ -586,6 +592,5 @@ extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_r
   }
   mass_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, p);
   HCADSA_TRY(launch_status());
-  add_kernel<<<pairs, kKeys, 0, as_stream(stream)>>>(p, pairs);
-  return launch_status();
+  return launch_after(add_kernel, dim3(pairs), kKeys, as_stream(stream), p, pairs);
 }

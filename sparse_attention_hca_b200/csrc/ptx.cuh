@@ -389,6 +389,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          | (static_cast<uint32_t>(M >> 4) << 24);     // M / 16
 }
 
+// ------------------------------------------------------------------ programmatic dependent launch
+
+// The kernel launched after this one may start once every CTA has come here (or ended) ...
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// ... and waits here until this one is complete and its writes are visible.
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ small numeric helpers
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
