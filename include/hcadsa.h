@@ -381,7 +381,7 @@ hcadsa_status mla_cache_append(const hcadsa_bf16* K, const hcadsa_bf16* V, long 
  * included).
  *   Q   : [T, Hq, 256] bf16, tokens q_row_stride elements apart (a multiple of 8)
  *   O   : [T, Hq, 256] bf16 (written for the tokens of the batch); lse: [T, Hq] fp32 or NULL
- *   workspace : mla_paged_attn_fwd_workspace_size(...) bytes, 16-byte aligned, scratch: calls that
+ *   workspace : mla_paged_attn_fwd_workspace_size(...) bytes, 32-byte aligned, scratch: calls that
  *               share it must be serialised.  The size depends on the current device's SM count.
  * scale > 0 (HCADSA_ERR_SHAPE otherwise).  Results do not depend on timing.
  */
@@ -400,7 +400,7 @@ hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_row_stride, c
  * other sequences keep theirs.  Deterministic as long as no page belongs to two sequences of the
  * batch (a shared row gets the sum of both, in either order).
  *   lse : [T, Hq] fp32;  mass : [n_pages, page, Hkv] fp32 (accumulated)
- *   workspace : as for the attention, mla_paged_attn_mass_workspace_size(...) bytes
+ *   workspace : as for the attention, mla_paged_attn_mass_workspace_size(...) bytes, 16-byte aligned
  */
 size_t mla_paged_attn_mass_workspace_size(int B, int T, int Hq, int Hkv);
 hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_row_stride, const hcadsa_bf16* K_pool,

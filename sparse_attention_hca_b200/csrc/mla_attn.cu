@@ -59,6 +59,7 @@ struct Params {
   int* ws_meta;  // [G][kMetaInts]
   int Hq, Hkv, g_log2, box_log2;
   float scale_log2;
+  bool wide_stores;  // O is 32-byte aligned
 };
 
 // A worker is a CTA pair or a single CTA.
@@ -253,6 +254,12 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
     if (done > lo) break;
   }
   __syncthreads();
+}
+
+__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -632,25 +639,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld_half32<128>(t_lanes + c * 32, o);
-          tmem_wait_ld_regs(o);
+        for (int c0 = 0; c0 < 4; c0 += 2) {  // 64 columns in flight: a TMEM load takes about 600 cycles
+          uint32_t o[2][32];
+          tmem_ld_half32<128>(t_lanes + c0 * 32, o[0]);
+          tmem_ld_half32<128>(t_lanes + c0 * 32 + 32, o[1]);
+          tmem_wait_ld_regs2(o[0], o[1]);
+          // whole 32-byte sectors per thread: half of one, as 16-byte stores write them, costs as much
           if (valid && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.O + orow * kMlaD + hf * 128 + c * 32);
+            uint16_t* dst = p.O + orow * kMlaD + hf * 128 + c0 * 32;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              uint4 v;
-              v.x = pack_bf16x2(__uint_as_float(o[8 * x + 0]) * inv, __uint_as_float(o[8 * x + 1]) * inv);
-              v.y = pack_bf16x2(__uint_as_float(o[8 * x + 2]) * inv, __uint_as_float(o[8 * x + 3]) * inv);
-              v.z = pack_bf16x2(__uint_as_float(o[8 * x + 4]) * inv, __uint_as_float(o[8 * x + 5]) * inv);
-              v.w = pack_bf16x2(__uint_as_float(o[8 * x + 6]) * inv, __uint_as_float(o[8 * x + 7]) * inv);
-              dst[x] = v;
+              uint32_t v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const uint32_t* q = &o[x >> 1][16 * (x & 1) + 2 * y];
+                v[y] = pack_bf16x2(__uint_as_float(q[0]) * inv, __uint_as_float(q[1]) * inv);
+              }
+              if (p.wide_stores) {
+                store_32(dst + 16 * x, v);
+              } else {
+                reinterpret_cast<uint4*>(dst + 16 * x)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<uint4*>(dst + 16 * x)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+              }
             }
           } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.ws_O + ((size_t)slot * Sh::kRows + row) * kMlaD + hf * 128 + c * 32);
+            float* dst = p.ws_O + ((size_t)slot * Sh::kRows + row) * kMlaD + hf * 128 + c0 * 32;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 8; ++x) {
+              uint32_t v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) v[y] = o[x >> 2][8 * (x & 3) + y];
+              store_32(dst + 8 * x, v);
+            }
           }
           __syncwarp();
         }
@@ -849,7 +869,7 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
   const int sms = sms_of_device();
   if (sms <= 0) return HCADSA_ERR_CUDA;
   if (!workspace || workspace_bytes < workspace_bytes_of(sms)) return HCADSA_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return HCADSA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(workspace) & 31u) return HCADSA_ERR_ALIGN;
   Params p;
   p.s = paged_batch(table, cu_q, kv_len, B, T, n_pages, page, max_pages);
   p.O = O;
@@ -862,6 +882,7 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
   p.g_log2 = log2_of(Hq / Hkv);
   p.box_log2 = page < 64 ? log2_of(page) : 6;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.wide_stores = (reinterpret_cast<uintptr_t>(O) & 31u) == 0;
   CUtensorMap mq, mk, mv;
   {
     const int g = 1 << p.g_log2;
