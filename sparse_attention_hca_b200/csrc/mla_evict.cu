@@ -6,16 +6,20 @@
 // touched; the i-th row that stays beyond it moves to the i-th freed place below it, so a cut of
 // m rows moves at most m rows, whatever the budget.
 //
-// One cluster of 1 to 8 CTAs per (sequence, K/V head); a CTA owns a contiguous slice of the rows.
-//   * Weights become 32-bit keys whose order is that of the weights (protected rows on top) and
-//     stay in shared memory.  The budget-th largest key is found with a radix select of 11, 11
-//     and 10 bits: a histogram per CTA, summed over the cluster through distributed shared
-//     memory, so all CTAs follow the same bin.
-//   * Ties at the threshold are taken in row order: every warp owns a contiguous run of its
-//     CTA's slice, and prefix counts over warps and CTAs give each row its rank, with no atomics:
-//     the result does not depend on timing.
-// Slices that do not fit in shared memory (caches of more than 8 * 48K rows) are read from
-// global memory again in every pass.
+// One cluster of 2 to 8 CTAs per (sequence, K/V head).  The first CTAs share the rows below the
+// budget, the others those beyond it, in contiguous slices, so every CTA counts either freed places
+// or rows that move.
+//   * Weights become 32-bit keys whose order is that of the weights (protected rows on top) and stay
+//     in shared memory.  The budget-th largest key is found with a radix select of 11, 11 and 10
+//     bits: a histogram per CTA and pass, read by all CTAs of the cluster through distributed shared
+//     memory, so all follow the same bin, with one cluster barrier per pass.
+//   * The same histograms say how many rows of every CTA lie above the threshold and how many equal
+//     it.  Ties are taken in row order: from those counts, and counts per warp (a warp owns a
+//     contiguous run of its CTA's slice), every row knows its rank.  No atomics decide anything that
+//     is written: the result does not depend on timing.
+// What bounds it is latency: two dependent loads per row, three passes over the keys, four cluster
+// barriers.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
+// do not fit in shared memory are read from global memory again in every pass.
 #include "mla_host.h"
 #include "pair.cuh"
 
@@ -36,17 +40,21 @@ struct Params {
   int2* moves;
   int32_t* new_len;
   int Hkv, budget, n_sink, n_recent, n_moves;
-  int smem_rows;  // rows of a slice that fit the dynamic shared memory; 0: keys are recomputed
+  int smem_rows;  // rows of a slice that fit the dynamic shared memory
+  bool vec;       // four rows are 16 aligned bytes of mass and pos
 };
 
 struct Shared {
-  uint32_t hist[kBins];    // this CTA's counts (read by the cluster)
+  uint32_t hist[3][kBins];       // this CTA's counts of each pass (read by the cluster)
   uint32_t warp_sum[32];
-  uint32_t digit, above;   // found by one thread of every CTA
-  uint32_t total[2];       // this CTA's counts of a pass (read by the cluster)
+  uint32_t digit, above;         // the bin of a pass, and the rows above it, found by one thread
+  uint32_t gt[kMaxCluster];      // rows above the threshold, by CTA
+  uint32_t eq[kMaxCluster];      // rows that equal it
+  uint32_t warp_gt[32], warp_eq[32];
 };
 
-// Keys in the order of the weights: protected rows over everything, NaN over +inf, -0 equal to 0.
+// Keys in the order of the weights: protected rows over everything, NaN over +inf, -0 equal to 0.  No
+// key is 0, which stands for a row that is not there.
 __device__ __forceinline__ uint32_t key_of(float m, bool safe) {
   if (safe) return 0xffffffffu;
   if (m != m) return 0xfffffffeu;
@@ -64,173 +72,225 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x, int lane) {
 }
 
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ uint4 keys[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t n_cta;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
-  const uint32_t rank = cluster_rank();
+  uint32_t n_cta_;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta_));
+  const int n_cta = (int)n_cta_, rank = (int)cluster_rank();
   const int list = blockIdx.x / n_cta;
   const int b = list / p.Hkv, h = list - b * p.Hkv;
+  const int budget = p.budget;
   const int len = paged_len(p.s, b, h == 0 && rank == 0 && tid == 0);
   int2* out = p.moves + (size_t)list * p.n_moves;
-  if (h == 0 && rank == 0 && tid == 0) p.new_len[b] = min(len, p.budget);
-  if (len <= p.budget) {  // nothing to evict
+  if (h == 0 && rank == 0 && tid == 0) p.new_len[b] = min(len, budget);
+  if (len <= budget) {  // nothing to evict
     for (int i = rank * kThreads + tid; i < p.n_moves; i += n_cta * kThreads) out[i] = make_int2(-1, -1);
     return;
   }
-  // rows [lo, hi) of this CTA; warp w owns rows [lo + w * per_warp, ...)
-  const int per_cta = ((len + (int)n_cta - 1) / (int)n_cta + kThreads - 1) / kThreads * kThreads;
-  const int lo = min(len, (int)rank * per_cta), hi = min(len, lo + per_cta);
-  const int per_warp = per_cta / 32;
-  const int w_lo = min(hi, lo + warp * per_warp), w_hi = min(hi, w_lo + per_warp);
-  const bool in_smem = per_cta <= p.smem_rows;
+  // CTAs [0, c1) share the rows [0, budget), the others [budget, len); slices start at multiples of 4
+  // from the start of their side, the second side's start rounded down (row_of).
+  int c1 = (int)(((long long)n_cta * budget + len / 2) / len);
+  c1 = c1 < 1 ? 1 : (c1 > n_cta - 1 ? n_cta - 1 : c1);
+  const int a0 = budget & ~3;
+  const int per1 = ((budget + c1 - 1) / c1 + 3) & ~3, per2 = ((len - a0 + n_cta - c1 - 1) / (n_cta - c1) + 3) & ~3;
+  auto slice = [&](int r, int& start, int& lo, int& hi) {  // start: multiple of 4; rows [lo, hi)
+    start = r < c1 ? r * per1 : a0 + (r - c1) * per2;
+    lo = r < c1 ? min(start, budget) : min(max(start, budget), len);
+    hi = r < c1 ? min(start + per1, budget) : min(start + per2, len);
+    if (hi < lo) hi = lo;
+  };
+  int start, lo, hi;
+  slice(rank, start, lo, hi);
+  const bool late_side = rank >= c1;
+  const int quads = hi > lo ? (hi - start + 3) / 4 : 0;  // groups of four rows of this CTA
+  const bool in_smem = 4 * quads <= p.smem_rows;
   const long long seen = p.seen ? p.seen[b] : len;
   const int page_mask = (1 << p.s.page_log2) - 1;
 
-  auto load_key = [&](int i) -> uint32_t {
-    const int pg = paged_page(p.s, b, i);
-    if (pg < 0) return key_of(0.0f, false);
-    const size_t slot = (((size_t)pg << p.s.page_log2) + (i & page_mask)) * p.Hkv + h;
-    const int ps = p.pos[slot];
-    return key_of(p.mass[slot], ps < p.n_sink || ps >= seen - p.n_recent);
+  // four keys from four consecutive rows of page pg (-1: recorded as bad; its rows count as weightless)
+  auto load_keys = [&](int q, int pg) -> uint4 {
+    const int i = start + 4 * q;
+    uint32_t k[4];
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int ps[4];
+    const bool ok = pg >= 0;
+    if (ok) {
+      const size_t slot = (((size_t)pg << p.s.page_log2) + (i & page_mask)) * p.Hkv + h;
+      if (p.vec) {
+        const float4 m4 = *reinterpret_cast<const float4*>(p.mass + slot);
+        const int4 p4 = *reinterpret_cast<const int4*>(p.pos + slot);
+        m[0] = m4.x, m[1] = m4.y, m[2] = m4.z, m[3] = m4.w;
+        ps[0] = p4.x, ps[1] = p4.y, ps[2] = p4.z, ps[3] = p4.w;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          m[x] = p.mass[slot + (size_t)x * p.Hkv];
+          ps[x] = p.pos[slot + (size_t)x * p.Hkv];
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      k[x] = i + x < lo || i + x >= hi ? 0u : key_of(m[x], ok && (ps[x] < p.n_sink || ps[x] >= seen - p.n_recent));
+    return make_uint4(k[0], k[1], k[2], k[3]);
   };
+  auto page_at = [&](int q) { return paged_page(p.s, b, start + 4 * q); };
   if (in_smem) {
-#pragma unroll 4
-    for (int i = lo + tid; i < hi; i += kThreads) keys[i - lo] = load_key(i);
+    constexpr int kAhead = 4;  // page lookups, then row loads, in flight per thread
+    for (int q0 = tid; q0 < quads; q0 += kAhead * kThreads) {
+      int pg[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) pg[x] = q0 + x * kThreads < quads ? page_at(q0 + x * kThreads) : -1;
+      uint4 k[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (q0 + x * kThreads < quads) k[x] = load_keys(q0 + x * kThreads, pg[x]);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (q0 + x * kThreads < quads) keys[q0 + x * kThreads] = k[x];
+    }
   }
-  auto key_at = [&](int i) -> uint32_t { return in_smem ? keys[i - lo] : load_key(i); };
+  auto keys_at = [&](int q) -> uint4 { return in_smem ? keys[q] : load_keys(q, page_at(q)); };
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid < kMaxCluster) sh.gt[tid] = sh.eq[tid] = 0;
   __syncthreads();
 
   // ---- the budget-th largest key: `prefix` holds its bits found so far, `need` its rank among
   // the rows that share them
-  uint32_t prefix = 0, need = p.budget;
+  uint32_t prefix = 0, need = (uint32_t)budget;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
     const uint32_t mask = (1u << bits) - 1;
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-    __syncthreads();
-    for (int i0 = lo + (tid & ~31); i0 < hi; i0 += kThreads) {
-      const int i = i0 + lane;
-      const uint32_t k = i < hi ? key_at(i) : 0;
-      const bool in = i < hi && (pass == 0 || (k >> (shift + bits)) == prefix);
-      const uint32_t d = (k >> shift) & mask;
-      // rows of one bin in a whole warp (protected runs, ties) cost one atomic instead of 32
-      const uint32_t live = __ballot_sync(0xffffffffu, in);
-      if (!live) continue;
-      const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(live) - 1);
-      if (__all_sync(0xffffffffu, !in || d == d0)) {
-        if (lane == 0) atomicAdd(&sh.hist[d0], __popc(live));
-      } else if (in) {
-        atomicAdd(&sh.hist[d], 1u);
+    uint32_t* hist = sh.hist[pass];
+    for (int q0 = tid & ~31; q0 < quads; q0 += kThreads) {
+      const int q = q0 + lane;
+      const uint4 k4 = q < quads ? keys_at(q) : make_uint4(0, 0, 0, 0);
+      const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool in = kk[x] != 0 && (pass == 0 || (kk[x] >> (shift + bits)) == prefix);
+        const uint32_t d = (kk[x] >> shift) & mask;
+        // rows of one bin in a whole warp (protected runs, ties) cost one atomic instead of 32
+        const uint32_t live = __ballot_sync(0xffffffffu, in);
+        if (!live) continue;
+        const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(live) - 1);
+        if (__all_sync(0xffffffffu, !in || d == d0)) {
+          if (lane == 0) atomicAdd(&hist[d0], __popc(live));
+        } else if (in) {
+          atomicAdd(&hist[d], 1u);
+        }
       }
     }
     __syncthreads();
-    if (n_cta > 1) cluster_sync();
-    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-    uint32_t c0 = 0, c1 = 0;
-    for (uint32_t r = 0; r < n_cta; ++r) {
-      const uint32_t a = cluster_addr(&sh.hist[kBins - 2 - 2 * tid], r);
-      c1 += ld_cluster_u32(a);
-      c0 += ld_cluster_u32(a + 4);
+    cluster_sync();
+    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t, of every CTA
+    uint32_t c0[kMaxCluster], c1_[kMaxCluster], s0 = 0, s1 = 0;
+    const int bin0 = kBins - 1 - 2 * tid;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      c0[r] = c1_[r] = 0;
+      if (r < n_cta) {
+        const uint32_t a = cluster_addr(&hist[bin0 - 1], r);
+        c1_[r] = ld_cluster_u32(a);
+        c0[r] = ld_cluster_u32(a + 4);
+      }
     }
-    const uint32_t incl = warp_incl_scan(c0 + c1, lane);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) s0 += c0[r], s1 += c1_[r];
+    const uint32_t incl = warp_incl_scan(s0 + s1, lane);
     if (lane == 31) sh.warp_sum[warp] = incl;
     __syncthreads();
-    if (warp == 0) sh.warp_sum[lane] = warp_incl_scan(sh.warp_sum[lane], lane);
-    __syncthreads();
-    const uint32_t upto = incl + (warp ? sh.warp_sum[warp - 1] : 0), before = upto - c0 - c1;
+    const uint32_t sums = sh.warp_sum[lane];
+    const uint32_t sums_incl = warp_incl_scan(sums, lane);
+    const uint32_t upto = incl + __shfl_sync(0xffffffffu, sums_incl - sums, warp), before = upto - s0 - s1;
     if (before < need && need <= upto) {
-      const bool first = need <= before + c0;
-      sh.digit = kBins - 1 - 2 * tid - (first ? 0 : 1);
-      sh.above = before + (first ? 0 : c0);
+      const bool first = need <= before + s0;
+      sh.digit = (uint32_t)(first ? bin0 : bin0 - 1);
+      sh.above = before + (first ? 0 : s0);
     }
     __syncthreads();
-    prefix = (prefix << bits) | sh.digit;
+    const int digit = (int)sh.digit;
+    prefix = (prefix << bits) | (uint32_t)digit;
     need -= sh.above;
-    if (n_cta > 1) cluster_sync();  // the histograms have been read
-    else __syncthreads();
+    // per CTA: its rows above the bin, and in the last pass those in it
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= n_cta) break;
+      const uint32_t g = __reduce_add_sync(0xffffffffu, (bin0 > digit ? c0[r] : 0) + (bin0 - 1 > digit ? c1_[r] : 0));
+      if (lane == 0 && g) atomicAdd(&sh.gt[r], g);
+      if (pass == 2) {
+        if (bin0 == digit) sh.eq[r] = c0[r];
+        else if (bin0 - 1 == digit) sh.eq[r] = c1_[r];
+      }
+    }
   }
   const uint32_t thr = prefix;  // keys above it stay, and the first `need` rows that equal it
-
-  // ---- ties before this warp: counts of equal keys per warp, then over warps and CTAs
-  auto cta_prefix = [&](uint32_t mine, uint32_t& total) -> uint32_t {  // all warps; mine: uniform in a warp
-    if (lane == 0) sh.warp_sum[warp] = mine;
-    __syncthreads();
-    uint32_t x = sh.warp_sum[lane];
-    const uint32_t s = warp_incl_scan(x, lane);
-    total = __shfl_sync(0xffffffffu, s, 31);
-    const uint32_t before = __shfl_sync(0xffffffffu, s - x, warp);
-    __syncthreads();
-    return before;
-  };
-  uint32_t eq = 0;
-  for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-    const int i = i0 + lane;
-    eq += __popc(__ballot_sync(0xffffffffu, i < w_hi && key_at(i) == thr));
+  // ---- counts per warp: warp w owns the groups [w * per_warp, ...) of the CTA
+  const int per_warp = ((quads + 31) / 32 + 31) / 32 * 32;
+  const int w_lo = min(quads, warp * per_warp), w_hi = min(quads, w_lo + per_warp);
+  uint32_t n_gt = 0, n_eq = 0;
+  for (int q0 = w_lo; q0 < w_hi; q0 += 32) {
+    const int q = q0 + lane;
+    const uint4 k4 = q < w_hi ? keys_at(q) : make_uint4(0, 0, 0, 0);
+    n_gt += (k4.x > thr) + (k4.y > thr) + (k4.z > thr) + (k4.w > thr);
+    n_eq += (k4.x == thr) + (k4.y == thr) + (k4.z == thr) + (k4.w == thr);
   }
-  uint32_t total;
-  uint32_t eq_before = cta_prefix(eq, total);
-  if (n_cta > 1) {
-    if (tid == 0) sh.total[0] = total;
-    cluster_sync();
-    for (uint32_t r = 0; r < rank; ++r) eq_before += ld_cluster_u32(cluster_addr(&sh.total[0], r));
-    cluster_sync();
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+  if (lane == 0) {
+    sh.warp_gt[warp] = n_gt;
+    sh.warp_eq[warp] = n_eq;
   }
-  // ---- rows that stay beyond the budget and places freed below it, counted, then written
-  uint32_t late = 0, freed = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    uint32_t e = eq_before;
-    uint32_t n_late = late, n_free = freed;  // pass 1: ranks of this warp's first rows
-    for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t k = i < w_hi ? key_at(i) : 0;
-      const bool is_eq = i < w_hi && k == thr;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-      const uint32_t below = (1u << lane) - 1;
-      const bool keep = i < w_hi && (k > thr || (is_eq && e + __popc(eqs & below) < need));
-      e += __popc(eqs);
-      const uint32_t ls = __ballot_sync(0xffffffffu, keep && i >= p.budget);
-      const uint32_t fs = __ballot_sync(0xffffffffu, i < w_hi && !keep && i < p.budget);
-      if (pass) {
-        if ((ls >> lane) & 1u) {
-          const uint32_t at = n_late + __popc(ls & below);
-          if (at < (uint32_t)p.n_moves) out[at].x = i;
-        }
-        if ((fs >> lane) & 1u) {
-          const uint32_t at = n_free + __popc(fs & below);
-          if (at < (uint32_t)p.n_moves) out[at].y = i;
-        }
+  __syncthreads();
+  // ---- ranks: entries and ties before this CTA, then before this warp
+  uint32_t before_cta = 0, eq_run = 0, at = 0, total = 0;
+  for (int r = 0; r < n_cta; ++r) {
+    int s_, l_, h_;
+    slice(r, s_, l_, h_);
+    const uint32_t kept = sh.gt[r] + min(need, eq_run + sh.eq[r]) - min(need, eq_run);
+    const uint32_t entries = r >= c1 ? kept : (uint32_t)(h_ - l_) - kept;
+    if (r >= c1) total += entries;
+    if (r < rank && (r >= c1) == late_side) at += entries;
+    if (r == rank) before_cta = eq_run;
+    eq_run += sh.eq[r];
+  }
+  {
+    const uint32_t g = sh.warp_gt[lane], e = sh.warp_eq[lane];
+    const uint32_t g_before = __shfl_sync(0xffffffffu, warp_incl_scan(g, lane) - g, warp);
+    const uint32_t e_before = before_cta + __shfl_sync(0xffffffffu, warp_incl_scan(e, lane) - e, warp);
+    const uint32_t taken = min(need, e_before) - min(need, before_cta);
+    uint32_t kept = g_before + taken;  // staying rows of this CTA before the position reached
+    uint32_t ties = e_before;          // rows that equal the threshold before it, over the whole list
+    int32_t* dst = reinterpret_cast<int32_t*>(out) + (late_side ? 0 : 1);
+    for (int q0 = w_lo; q0 < w_hi; q0 += 32) {
+      const int q = q0 + lane;
+      const uint4 k4 = q < w_hi ? keys_at(q) : make_uint4(0, 0, 0, 0);
+      const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+      uint32_t mine = 0;  // rows above the threshold, and from bit 16 on those that equal it
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mine += (kk[x] > thr ? 1u : 0u) + (kk[x] == thr ? 0x10000u : 0u);
+      const uint32_t incl = warp_incl_scan(mine, lane), excl = incl - mine;
+      uint32_t e = ties + (excl >> 16);
+      uint32_t k = kept + (excl & 0xffffu) + min(need, e) - min(need, ties);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = start + 4 * q + x;
+        const bool is_eq = kk[x] == thr, keep = kk[x] > thr || (is_eq && e < need);
+        const uint32_t entry = at + (late_side ? k : (uint32_t)(i - lo) - k);
+        if (kk[x] != 0 && keep == late_side && entry < (uint32_t)p.n_moves) dst[2 * (size_t)entry] = i;
+        e += is_eq;
+        k += keep;
       }
-      n_late += __popc(ls);
-      n_free += __popc(fs);
+      const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+      kept += (all & 0xffffu) + min(need, ties + (all >> 16)) - min(need, ties);
+      ties += all >> 16;
     }
-    if (pass) break;
-    uint32_t t_late, t_free;
-    late = cta_prefix(n_late, t_late);
-    freed = cta_prefix(n_free, t_free);
-    if (n_cta > 1) {
-      if (tid == 0) {
-        sh.total[0] = t_late;
-        sh.total[1] = t_free;
-      }
-      cluster_sync();
-      t_late = 0;
-      for (uint32_t r = 0; r < n_cta; ++r) {
-        const uint32_t l = ld_cluster_u32(cluster_addr(&sh.total[0], r));
-        if (r < rank) {
-          late += l;
-          freed += ld_cluster_u32(cluster_addr(&sh.total[1], r));
-        }
-        t_late += l;
-      }
-      cluster_sync();  // no CTA ends while another reads its counts
-    }
-    for (int i = t_late + rank * kThreads + tid; i < p.n_moves; i += n_cta * kThreads) out[i] = make_int2(-1, -1);
   }
+  for (int i = (int)total + rank * kThreads + tid; i < p.n_moves; i += n_cta * kThreads) out[i] = make_int2(-1, -1);
+  cluster_sync();  // no CTA ends while another reads its histograms
 }
 
 }  // namespace
@@ -251,11 +311,12 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
       (reinterpret_cast<uintptr_t>(moves) & 7u) || !aligned4(new_len))
     return HCADSA_ERR_ALIGN;
   if (B == 0) return HCADSA_OK;
-  int cluster = 1;
+  int cluster = 2;
   while (cluster < kMaxCluster && cap > (long long)cluster * kSliceTarget) cluster *= 2;
   const long long blocks = (long long)B * Hkv * cluster;
   if (blocks > 2147483647LL) return HCADSA_ERR_UNSUPPORTED;
-  const long long slice = ((cap + cluster - 1) / cluster + kThreads - 1) / kThreads * kThreads;
+  // a side's share of the CTAs is rounded, so a slice may be half as long again as the average
+  const long long slice = (cap * 3 / 2 / cluster + 64 + 3) / 4 * 4;
   Params p;
   p.s = paged_batch(table, nullptr, kv_len, B, 0, n_pages, page, max_pages);
   p.mass = mass;
@@ -268,9 +329,10 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   p.n_sink = n_sink;
   p.n_recent = n_recent;
   p.n_moves = n_moves;
-  p.smem_rows = slice <= kMaxSmemRows ? (int)slice : 0;
+  p.smem_rows = (int)(slice < kMaxSmemRows ? slice : kMaxSmemRows);
+  p.vec = Hkv == 1 && aligned16(mass) && aligned16(pos);
   const size_t smem = (size_t)p.smem_rows * 4;
-  if (smem > 32 * 1024 && cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 16 * 1024 && cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kMaxSmemRows * 4) != cudaSuccess)
     return launch_status();
   cudaLaunchConfig_t cfg = {};
