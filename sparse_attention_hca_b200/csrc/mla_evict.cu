@@ -11,26 +11,30 @@
 // or rows that move.
 //   * Weights become 32-bit keys whose order is that of the weights (protected rows on top) and stay
 //     in shared memory.  The budget-th largest key is found with a radix select of 11, 11 and 10
-//     bits: a histogram per CTA and pass, read by all CTAs of the cluster through distributed shared
-//     memory, so all follow the same bin, with one cluster barrier per pass.
-//   * The same histograms say how many rows of every CTA lie above the threshold and how many equal
-//     it.  Ties are taken in row order: from those counts, and counts per warp (a warp owns a
-//     contiguous run of its CTA's slice), every row knows its rank.  No atomics decide anything that
-//     is written: the result does not depend on timing.
+//     bits: a histogram per CTA and pass, with one cluster barrier per pass.  One warp of every CTA
+//     then reads, through distributed shared memory, 64 sums of 32 bins from each CTA, and the 32
+//     bins of the group that holds the rank: all CTAs follow the same bin, and a pass moves 768
+//     words per CTA instead of whole histograms (8 x 2048 words took 9000 cycles).
+//   * Ties at the threshold are taken in row order: from counts per warp (a warp owns a contiguous run
+//     of its CTA's slice) and per CTA every row knows its rank.  No atomics decide anything that is
+//     written: the result does not depend on timing.
+//   * Entries are gathered in shared memory, 128 rows of a warp at a time, and written side by side.
 // What bounds it is latency: two dependent loads per row, three passes over the keys, four cluster
 // barriers.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
 // do not fit in shared memory are read from global memory again in every pass.
+#include <mutex>
+
 #include "mla_host.h"
 #include "pair.cuh"
 
 namespace hcadsa {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSliceTarget = 4096;     // rows per CTA below which a list gets no further CTA
-constexpr int kMaxSmemRows = 48 * 1024;
+constexpr int kGroupBins = 32, kBinGroups = kBins / kGroupBins;
+constexpr int kMaxSmemRows = 44 * 1024;
+constexpr uint32_t kSafe = 0xffffffffu;  // the key of a protected row
 
 struct Params {
   PagedBatch s;
@@ -44,19 +48,21 @@ struct Params {
   bool vec;       // four rows are 16 aligned bytes of mass and pos
 };
 
+template <int kWarps>
 struct Shared {
-  uint32_t hist[3][kBins];       // this CTA's counts of each pass (read by the cluster)
-  uint32_t warp_sum[32];
-  uint32_t digit, above;         // the bin of a pass, and the rows above it, found by one thread
-  uint32_t gt[kMaxCluster];      // rows above the threshold, by CTA
-  uint32_t eq[kMaxCluster];      // rows that equal it
-  uint32_t warp_gt[32], warp_eq[32];
+  uint32_t hist[3][kBins];        // this CTA's counts of each pass (read by the cluster)
+  uint32_t group[3][kBinGroups];  // and of every 32 bins (read by the cluster)
+  uint32_t protected_rows;        // (read by the cluster)
+  uint32_t total[2];              // rows above the threshold, rows that equal it (read by the cluster)
+  uint32_t digit, need;           // the bin of a pass, and the rank left among its rows
+  uint32_t warp_gt[kWarps], warp_eq[kWarps];
+  int32_t entry[kWarps][128];     // a warp's next entries of the list
 };
 
 // Keys in the order of the weights: protected rows over everything, NaN over +inf, -0 equal to 0.  No
 // key is 0, which stands for a row that is not there.
 __device__ __forceinline__ uint32_t key_of(float m, bool safe) {
-  if (safe) return 0xffffffffu;
+  if (safe) return kSafe;
   if (m != m) return 0xfffffffeu;
   const uint32_t u = __float_as_uint(m + 0.0f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
@@ -71,9 +77,11 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x, int lane) {
   return x;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint4 keys[];
-  __shared__ Shared sh;
+  __shared__ Shared<kWarps> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t n_cta_;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta_));
@@ -153,83 +161,90 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
   }
   auto keys_at = [&](int q) -> uint4 { return in_smem ? keys[q] : load_keys(q, page_at(q)); };
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid < kMaxCluster) sh.gt[tid] = sh.eq[tid] = 0;
+  if (tid == 0) sh.protected_rows = 0;
   __syncthreads();
 
-  // ---- the budget-th largest key: `prefix` holds its bits found so far, `need` its rank among
-  // the rows that share them
+  // ---- the budget-th largest key: `prefix` holds its bits found so far, `need` its rank among the
+  // rows that share them.  Protected rows, which come in runs, are counted without the histogram.
   uint32_t prefix = 0, need = (uint32_t)budget;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const int bits = pass == 2 ? 10 : 11;
-    const uint32_t mask = (1u << bits) - 1;
     uint32_t* hist = sh.hist[pass];
-    for (int q0 = tid & ~31; q0 < quads; q0 += kThreads) {
-      const int q = q0 + lane;
-      const uint4 k4 = q < quads ? keys_at(q) : make_uint4(0, 0, 0, 0);
+    uint32_t safe = 0;
+    for (int q = tid; q < quads; q += kThreads) {
+      const uint4 k4 = keys_at(q);
       const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const bool in = kk[x] != 0 && (pass == 0 || (kk[x] >> (shift + bits)) == prefix);
-        const uint32_t d = (kk[x] >> shift) & mask;
-        // rows of one bin in a whole warp (protected runs, ties) cost one atomic instead of 32
-        const uint32_t live = __ballot_sync(0xffffffffu, in);
-        if (!live) continue;
-        const uint32_t d0 = __shfl_sync(0xffffffffu, d, __ffs(live) - 1);
-        if (__all_sync(0xffffffffu, !in || d == d0)) {
-          if (lane == 0) atomicAdd(&hist[d0], __popc(live));
-        } else if (in) {
-          atomicAdd(&hist[d], 1u);
+        if (pass == 0) {
+          if (kk[x] == kSafe) ++safe;
+          else if (kk[x] != 0) atomicAdd(&hist[kk[x] >> 21], 1u);
+        } else if ((kk[x] >> (shift + bits)) == prefix && kk[x] != kSafe) {
+          atomicAdd(&hist[(kk[x] >> shift) & ((1u << bits) - 1)], 1u);
         }
       }
     }
+    if (pass == 0) {
+      safe = __reduce_add_sync(0xffffffffu, safe);
+      if (lane == 0) atomicAdd(&sh.protected_rows, safe);
+    }
+    __syncthreads();
+    for (int g = warp; g < kBinGroups; g += kWarps) {
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, hist[g * kGroupBins + lane]);
+      if (lane == 0) sh.group[pass][g] = sum;
+    }
     __syncthreads();
     cluster_sync();
-    // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t, of every CTA
-    uint32_t c0[kMaxCluster], c1_[kMaxCluster], s0 = 0, s1 = 0;
-    const int bin0 = kBins - 1 - 2 * tid;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      c0[r] = c1_[r] = 0;
-      if (r < n_cta) {
-        const uint32_t a = cluster_addr(&hist[bin0 - 1], r);
-        c1_[r] = ld_cluster_u32(a);
-        c0[r] = ld_cluster_u32(a + 4);
+    if (warp == 0) {
+      if (pass == 0) {
+        const uint32_t mine = ld_cluster_u32(cluster_addr(&sh.protected_rows, lane < n_cta ? lane : rank));
+        const uint32_t all = __reduce_add_sync(0xffffffffu, lane < n_cta ? mine : 0);
+        need = all < need ? need - all : 0;  // 0: the budget goes to protected rows alone
       }
-    }
+      // from the top: lane l holds the groups 63 - 2 l and 62 - 2 l, then the bin 31 - l of the group that
+      // holds the rank (unconditional loads from every CTA, all in flight at once)
+      const int g0 = kBinGroups - 1 - 2 * lane;
+      uint32_t s0 = 0, s1 = 0;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) s0 += c0[r], s1 += c1_[r];
-    const uint32_t incl = warp_incl_scan(s0 + s1, lane);
-    if (lane == 31) sh.warp_sum[warp] = incl;
-    __syncthreads();
-    const uint32_t sums = sh.warp_sum[lane];
-    const uint32_t sums_incl = warp_incl_scan(sums, lane);
-    const uint32_t upto = incl + __shfl_sync(0xffffffffu, sums_incl - sums, warp), before = upto - s0 - s1;
-    if (before < need && need <= upto) {
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const uint32_t a = cluster_addr(&sh.group[pass][g0 - 1], r < n_cta ? r : rank);
+        const uint32_t c_lo = ld_cluster_u32(a), c_hi = ld_cluster_u32(a + 4);
+        s1 += r < n_cta ? c_lo : 0;
+        s0 += r < n_cta ? c_hi : 0;
+      }
+      const uint32_t upto = warp_incl_scan(s0 + s1, lane), before = upto - s0 - s1;
+      const int at = __ffs(__ballot_sync(0xffffffffu, upto >= need)) - 1;  // the lane of the rank's group
       const bool first = need <= before + s0;
-      sh.digit = (uint32_t)(first ? bin0 : bin0 - 1);
-      sh.above = before + (first ? 0 : s0);
-    }
-    __syncthreads();
-    const int digit = (int)sh.digit;
-    prefix = (prefix << bits) | (uint32_t)digit;
-    need -= sh.above;
-    // per CTA: its rows above the bin, and in the last pass those in it
+      const uint32_t above0 = __shfl_sync(0xffffffffu, before + (first ? 0 : s0), at);
+      const int group = __shfl_sync(0xffffffffu, first ? g0 : g0 - 1, at);
+      uint32_t sum = 0;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      if (r >= n_cta) break;
-      const uint32_t g = __reduce_add_sync(0xffffffffu, (bin0 > digit ? c0[r] : 0) + (bin0 - 1 > digit ? c1_[r] : 0));
-      if (lane == 0 && g) atomicAdd(&sh.gt[r], g);
-      if (pass == 2) {
-        if (bin0 == digit) sh.eq[r] = c0[r];
-        else if (bin0 - 1 == digit) sh.eq[r] = c1_[r];
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const uint32_t c = ld_cluster_u32(cluster_addr(&hist[group * kGroupBins + 31 - lane], r < n_cta ? r : rank));
+        sum += r < n_cta ? c : 0;
+      }
+      const uint32_t incl = above0 + warp_incl_scan(sum, lane);
+      const int in_group = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+      const uint32_t above = __shfl_sync(0xffffffffu, incl - sum, in_group);
+      if (lane == 0) {
+        sh.digit = (uint32_t)(group * kGroupBins + 31 - in_group);
+        sh.need = need - (need ? above : 0);
       }
     }
+    __syncthreads();
+    prefix = (prefix << bits) | sh.digit;
+    need = sh.need;
+    if (need == 0) break;  // (in the first pass only: every later rank is at least 1)
+  }
+  if (need == 0) {
+    prefix = kSafe;
+    need = (uint32_t)budget;
   }
   const uint32_t thr = prefix;  // keys above it stay, and the first `need` rows that equal it
   // ---- counts per warp: warp w owns the groups [w * per_warp, ...) of the CTA
-  const int per_warp = ((quads + 31) / 32 + 31) / 32 * 32;
+  const int per_warp = ((quads + kWarps - 1) / kWarps + 31) / 32 * 32;
   const int w_lo = min(quads, warp * per_warp), w_hi = min(quads, w_lo + per_warp);
   uint32_t n_gt = 0, n_eq = 0;
   for (int q0 = w_lo; q0 < w_hi; q0 += 32) {
@@ -245,20 +260,33 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
     sh.warp_eq[warp] = n_eq;
   }
   __syncthreads();
-  // ---- ranks: entries and ties before this CTA, then before this warp
-  uint32_t before_cta = 0, eq_run = 0, at = 0, total = 0;
-  for (int r = 0; r < n_cta; ++r) {
+  if (warp == 0) {
+    const uint32_t g = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_gt[lane] : 0);
+    const uint32_t e = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.warp_eq[lane] : 0);
+    if (lane == 0) {
+      sh.total[0] = g;
+      sh.total[1] = e;
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  // ---- ranks: entries and ties before this CTA (lane r reads CTA r's counts), then before this warp
+  uint32_t before_cta, at, total;
+  {
+    const int r = lane < n_cta ? lane : rank;
+    const uint32_t a = cluster_addr(&sh.total[0], r);
+    const uint32_t g = lane < n_cta ? ld_cluster_u32(a) : 0, e = lane < n_cta ? ld_cluster_u32(a + 4) : 0;
+    const uint32_t e_to = warp_incl_scan(e, lane), e_from = e_to - e;
+    const uint32_t kept = g + min(need, e_to) - min(need, e_from);
     int s_, l_, h_;
     slice(r, s_, l_, h_);
-    const uint32_t kept = sh.gt[r] + min(need, eq_run + sh.eq[r]) - min(need, eq_run);
-    const uint32_t entries = r >= c1 ? kept : (uint32_t)(h_ - l_) - kept;
-    if (r >= c1) total += entries;
-    if (r < rank && (r >= c1) == late_side) at += entries;
-    if (r == rank) before_cta = eq_run;
-    eq_run += sh.eq[r];
+    const uint32_t entries = lane >= n_cta ? 0 : (lane >= c1 ? kept : (uint32_t)(h_ - l_) - kept);
+    before_cta = __shfl_sync(0xffffffffu, e_from, rank);
+    at = __reduce_add_sync(0xffffffffu, lane < rank && (lane >= c1) == late_side ? entries : 0);
+    total = __reduce_add_sync(0xffffffffu, lane >= c1 ? entries : 0);
   }
   {
-    const uint32_t g = sh.warp_gt[lane], e = sh.warp_eq[lane];
+    const uint32_t g = lane < kWarps ? sh.warp_gt[lane] : 0, e = lane < kWarps ? sh.warp_eq[lane] : 0;
     const uint32_t g_before = __shfl_sync(0xffffffffu, warp_incl_scan(g, lane) - g, warp);
     const uint32_t e_before = before_cta + __shfl_sync(0xffffffffu, warp_incl_scan(e, lane) - e, warp);
     const uint32_t taken = min(need, e_before) - min(need, before_cta);
@@ -275,22 +303,59 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
       const uint32_t incl = warp_incl_scan(mine, lane), excl = incl - mine;
       uint32_t e = ties + (excl >> 16);
       uint32_t k = kept + (excl & 0xffffu) + min(need, e) - min(need, ties);
+      // entries before this step of the warp: staying rows, or freed places
+      const int row0 = max(start + 4 * q0, lo);
+      const uint32_t first = late_side ? kept : (uint32_t)(row0 - lo) - kept;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = start + 4 * q + x;
         const bool is_eq = kk[x] == thr, keep = kk[x] > thr || (is_eq && e < need);
-        const uint32_t entry = at + (late_side ? k : (uint32_t)(i - lo) - k);
-        if (kk[x] != 0 && keep == late_side && entry < (uint32_t)p.n_moves) dst[2 * (size_t)entry] = i;
+        if (kk[x] != 0 && keep == late_side) sh.entry[warp][(late_side ? k : (uint32_t)(i - lo) - k) - first] = i;
         e += is_eq;
         k += keep;
       }
       const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
       kept += (all & 0xffffu) + min(need, ties + (all >> 16)) - min(need, ties);
       ties += all >> 16;
+      const int row1 = min(start + 4 * q0 + 128, hi);
+      const uint32_t n = (late_side ? kept : (uint32_t)(row1 - lo) - kept) - first;
+      __syncwarp();
+      for (uint32_t o = lane; o < n; o += 32)
+        if (at + first + o < (uint32_t)p.n_moves) dst[2 * (size_t)(at + first + o)] = sh.entry[warp][o];
+      __syncwarp();
     }
   }
   for (int i = (int)total + rank * kThreads + tid; i < p.n_moves; i += n_cta * kThreads) out[i] = make_int2(-1, -1);
   cluster_sync();  // no CTA ends while another reads its histograms
+}
+
+// SMs of the current device, the kernels' shared memory set up.
+int sms_of_device() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!cache[dev]) {
+    int sms = 0;
+    const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(select_kernel<512>, most, kMaxSmemRows * 4) != cudaSuccess ||
+        cudaFuncSetAttribute(select_kernel<1024>, most, kMaxSmemRows * 4) != cudaSuccess) {
+      launch_status();
+      return 0;
+    }
+    cache[dev] = sms;
+  }
+  return cache[dev];
+}
+
+// A list of 4096 rows takes 12.4 us on four CTAs and 18.5 on two (32 lists at once); CTAs beyond one
+// per SM would wait for the first (35 us on eight).
+int cluster_of(long long lists, long long cap, int sms) {
+  int cluster = 2;
+  while (cluster < kMaxCluster && cap > 1024LL * cluster && 2 * cluster * lists <= sms) cluster *= 2;
+  return cluster;
 }
 
 }  // namespace
@@ -311,8 +376,9 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
       (reinterpret_cast<uintptr_t>(moves) & 7u) || !aligned4(new_len))
     return HCADSA_ERR_ALIGN;
   if (B == 0) return HCADSA_OK;
-  int cluster = 2;
-  while (cluster < kMaxCluster && cap > (long long)cluster * kSliceTarget) cluster *= 2;
+  const int sms = sms_of_device();
+  if (sms <= 0) return HCADSA_ERR_CUDA;
+  const int cluster = cluster_of((long long)B * Hkv, cap, sms);
   const long long blocks = (long long)B * Hkv * cluster;
   if (blocks > 2147483647LL) return HCADSA_ERR_UNSUPPORTED;
   // a side's share of the CTAs is rounded, so a slice may be half as long again as the average
@@ -332,12 +398,11 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   p.smem_rows = (int)(slice < kMaxSmemRows ? slice : kMaxSmemRows);
   p.vec = Hkv == 1 && aligned16(mass) && aligned16(pos);
   const size_t smem = (size_t)p.smem_rows * 4;
-  if (smem > 16 * 1024 && cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxSmemRows * 4) != cudaSuccess)
-    return launch_status();
+  // 4096 rows per CTA and list: 512 threads 12.4 us, 1024 threads 14.4; 16384 rows: 28.7 and 26.8
+  const bool wide = cap > 8192LL * cluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.blockDim = dim3(wide ? 1024 : 512, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = as_stream(stream);
   cudaLaunchAttribute attr[1];
@@ -347,6 +412,6 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, select_kernel, p) != cudaSuccess) return launch_status();
+  if (cudaLaunchKernelEx(&cfg, wide ? select_kernel<1024> : select_kernel<512>, p) != cudaSuccess) return launch_status();
   return launch_status();
 }
