@@ -28,10 +28,27 @@ struct AppendParams {
 };
 
 // A block owns kTokens packed tokens: all its threads look for the sequences that own them (one
-// pass over cu_q, no search chain), then a warp copies one (token, head) at a time.
+// pass over cu_q, no search chain) while the first K and V rows are on their way, one thread per
+// token looks up where it goes, and the warps copy one (token, head) after the other, kAhead rows
+// of each pool in flight.
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams p) {
   __shared__ int owner[kTokens];
+  __shared__ int page_of[kTokens], place_of[kTokens];  // where the token's row goes; page -1: nowhere
   const int t0 = blockIdx.x * kTokens, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int units = min(kTokens, p.s.T - t0) * p.Hkv;
+  constexpr int kAhead = 4;
+  uint4 k[kAhead], v[kAhead];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int u = u0 + x * kWarps;
+      if (u >= units) continue;
+      const int i = u / p.Hkv, h = u - i * p.Hkv;
+      k[x] = reinterpret_cast<const uint4*>(p.K + (size_t)(t0 + i) * p.k_row + (size_t)h * kMlaD)[lane];
+      v[x] = reinterpret_cast<const uint4*>(p.V + (size_t)(t0 + i) * p.v_row + (size_t)h * kMlaD)[lane];
+    }
+  };
+  load(warp);
   if (threadIdx.x < kTokens) owner[threadIdx.x] = -1;
   __syncthreads();
   for (int b = threadIdx.x; b < p.s.B; b += blockDim.x) {
@@ -40,30 +57,41 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
     for (int t = a; t < z; ++t) owner[t - t0] = b;
   }
   __syncthreads();
-  const int n_tok = min(kTokens, p.s.T - t0);
   const int page_mask = (1 << p.s.page_log2) - 1;
-  for (int u = warp; u < n_tok * p.Hkv; u += kWarps) {
-    const int i = u / p.Hkv, h = u - i * p.Hkv, t = t0 + i;
-    const int b = owner[i];
-    if (b < 0) continue;  // a packed row behind the last sequence
-    const uint4 k = reinterpret_cast<const uint4*>(p.K + (size_t)t * p.k_row + (size_t)h * kMlaD)[lane];
-    const uint4 v = reinterpret_cast<const uint4*>(p.V + (size_t)t * p.v_row + (size_t)h * kMlaD)[lane];
-    const PagedSeq q = paged_seq(p.s, b, false);
-    const int back = q.q0 + q.n - t;  // rows from this one to the end
-    const int r = q.len - back;
-    if (r < 0) {  // the cache is declared shorter than the chunk
-      if (lane == 0) raise_device_error(p.s.err, kErrDeviceBounds);
-      continue;
+  if (threadIdx.x < kTokens) {
+    const int b = owner[threadIdx.x];
+    int pg = -1, r = 0;
+    if (b >= 0) {  // otherwise a packed row behind the last sequence
+      const PagedSeq q = paged_seq(p.s, b, false);
+      const int back = q.q0 + q.n - (t0 + (int)threadIdx.x);  // rows from this one to the end
+      r = q.len - back;
+      if (r >= 0) pg = paged_page(p.s, b, r);
+      else raise_device_error(p.s.err, kErrDeviceBounds);  // the cache is declared shorter than the chunk
+      if (pg >= 0) {
+        const size_t slot = (((size_t)pg << p.s.page_log2) + (r & page_mask)) * p.Hkv;
+        const int ps = p.seen ? p.seen[b] - back : r;
+        for (int h = 0; h < p.Hkv; ++h) {
+          if (p.pos) p.pos[slot + h] = ps;
+          if (p.mass) p.mass[slot + h] = 0.0f;
+        }
+      }
     }
-    const int pg = paged_page(p.s, b, r);
-    if (pg < 0) continue;
-    const int in = r & page_mask;
-    const size_t row = (size_t)in * p.Hkv + h;
-    reinterpret_cast<uint4*>(p.K_pool + (size_t)pg * p.k_page + row * kMlaD)[lane] = k;
-    reinterpret_cast<uint4*>(p.V_pool + (size_t)pg * p.v_page + row * kMlaD)[lane] = v;
-    const size_t slot = (((size_t)pg << p.s.page_log2) * p.Hkv) + row;
-    if (lane == 0 && p.pos) p.pos[slot] = p.seen ? p.seen[b] - back : r;
-    if (lane == 1 && p.mass) p.mass[slot] = 0.0f;
+    page_of[threadIdx.x] = pg;
+    place_of[threadIdx.x] = r & page_mask;
+  }
+  __syncthreads();
+  for (int u0 = warp; u0 < units; u0 += kAhead * kWarps) {
+    if (u0 != warp) load(u0);
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int u = u0 + x * kWarps;
+      if (u >= units) continue;
+      const int i = u / p.Hkv, h = u - i * p.Hkv, pg = page_of[i];
+      if (pg < 0) continue;
+      const size_t row = ((size_t)place_of[i] * p.Hkv + h) * kMlaD;
+      reinterpret_cast<uint4*>(p.K_pool + (size_t)pg * p.k_page + row)[lane] = k[x];
+      reinterpret_cast<uint4*>(p.V_pool + (size_t)pg * p.v_page + row)[lane] = v[x];
+    }
   }
 }
 
