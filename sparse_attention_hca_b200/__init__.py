@@ -580,17 +580,38 @@ def _need_exact(t, dtype, name, shape):
         _need(t, dtype, name, shape)
 
 
+def _need_pools(K_pool, V_pool):
+    """The two pools of a cache: their sizes and both page strides."""
+    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
+    if V_pool.dtype is torch.bfloat16 and V_pool.shape == K_pool.shape and V_pool.stride() == K_pool.stride():
+        return n_pages, page, Hkv, d, k_page, k_page
+    return n_pages, page, Hkv, d, k_page, _need_pool(V_pool, "V_pool", K_pool.shape)[4]
+
+
 def _need_batch(table, kv_len, cu_q=None, seen=None):
-    if table.dim() != 2:
-        raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
-    B, max_pages = table.shape
-    _need_exact(table, torch.int32, "table", (B, max_pages))
-    _need_exact(kv_len, torch.int32, "kv_len", (B,))
-    if cu_q is not None:
-        _need_exact(cu_q, torch.int32, "cu_q", (B + 1,))
-    if seen is not None:
-        _need_exact(seen, torch.int32, "seen", (B,))
+    shape = table.shape
+    if len(shape) != 2:
+        raise ValueError(f"table has shape {tuple(shape)}, expected [B, max_pages]")
+    B, max_pages = shape
+    i32 = torch.int32
+    # checked in place: these run once per call of a decode step
+    if not (table.dtype is i32 and table.is_contiguous() and kv_len.dtype is i32 and kv_len.shape == (B,) and
+            kv_len.is_contiguous()):
+        _need(table, i32, "table")
+        _need(kv_len, i32, "kv_len", (B,))
+    if cu_q is not None and not (cu_q.dtype is i32 and cu_q.shape == (B + 1,) and cu_q.is_contiguous()):
+        _need(cu_q, i32, "cu_q", (B + 1,))
+    if seen is not None and not (seen.dtype is i32 and seen.shape == (B,) and seen.is_contiguous()):
+        _need(seen, i32, "seen", (B,))
     return B, max_pages
+
+
+def _need_slots(pos, mass, shape):
+    """Positions and weights of every pool row; either may be None."""
+    if pos is not None and not (pos.dtype is torch.int32 and pos.shape == shape and pos.is_contiguous()):
+        _need(pos, torch.int32, "pos", shape)
+    if mass is not None and not (mass.dtype is torch.float32 and mass.shape == shape and mass.is_contiguous()):
+        _need(mass, torch.float32, "mass", shape)
 
 
 def _device_and_stream(stream, *tensors):
@@ -638,17 +659,13 @@ def mla_cache_append(K, V, K_pool, V_pool, table, cu_q, kv_len, *, seen=None, po
     in K_pool, V_pool [n_pages, page, Hkv, 256] (table [B, max_pages], cu_q [B + 1], kv_len [B] int32; kv_len counts
     the new rows).  pos (int32) and mass (fp32) [n_pages, page, Hkv], where given: pos = seen - n_b + i (seen: [B]
     int32, tokens so far; kv_len if None), mass = 0.  Returns (K_pool, V_pool)."""
-    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
+    n_pages, page, Hkv, d, k_page, v_page = _need_pools(K_pool, V_pool)
     T, _, dk, k_row = _need_rows(K, "K", Hkv)
     Tv, _, dv, v_row = _need_rows(V, "V", Hkv)
     if Tv != T or dk != d or dv != d:
         raise ValueError(f"K and V have shapes {tuple(K.shape)} and {tuple(V.shape)}, expected [T, {Hkv}, {d}] of one T")
     B, max_pages = _need_batch(table, kv_len, cu_q, seen)
-    if pos is not None:
-        _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
-    if mass is not None:
-        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _need_slots(pos, mass, (n_pages, page, Hkv))
     _, raw = _device_and_stream(stream, K, V, K_pool, V_pool, table, cu_q, kv_len, seen, pos, mass)
     st = lib().mla_cache_append(K.data_ptr(), V.data_ptr(), k_row, v_row, K_pool.data_ptr(), V_pool.data_ptr(), k_page,
                                 v_page, table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), _addr(seen), _addr(pos),
@@ -662,8 +679,7 @@ def mla_paged_attn_fwd(Q, K_pool, V_pool, table, cu_q, kv_len, *, scale: float |
     """Q: [T, Hq, 256], sequence b's new tokens at cu_q[b] .. cu_q[b+1]-1 -> O [T, Hq, 256] (and lse [T, Hq] fp32) over
     the kv_len[b] rows of its pages; new token i sees the rows <= kv_len[b] - n_b + i.  Pools, table and lengths as
     for mla_cache_append.  Rows of O and lse behind cu_q[B] are left as they are."""
-    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
+    n_pages, page, Hkv, d, k_page, v_page = _need_pools(K_pool, V_pool)
     T, Hq, dq, q_row = _need_rows(Q, "Q")
     if dq != d:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
@@ -697,8 +713,7 @@ def mla_paged_attn_mass(Q, K_pool, table, cu_q, kv_len, lse, *, scale: float | N
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [T, Hq, {d}]")
     B, max_pages = _need_batch(table, kv_len, cu_q)
     _need_exact(lse, torch.float32, "lse", (T, Hq))
-    if mass is not None:
-        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _need_slots(None, mass, (n_pages, page, Hkv))
     dev, raw = _device_and_stream(stream, Q, K_pool, table, cu_q, kv_len, lse, mass, workspace)
     if mass is None:
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
@@ -721,9 +736,8 @@ def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int
     mla_cache_move makes the moves."""
     if mass.dim() != 3:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected [n_pages, page, Hkv]")
-    n_pages, page, Hkv = mass.shape
-    _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
-    _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
+    n_pages, page, Hkv = shape = mass.shape
+    _need_slots(pos, mass, shape)
     B, max_pages = _need_batch(table, kv_len, seen=seen)
     n = max(0, min(budget, max_pages * page - budget))
     if moves is not None:
@@ -748,20 +762,16 @@ def mla_cache_move(moves, K_pool, V_pool, table, *, pos=None, mass=None, stream=
     """Copies pool rows within their sequences: for every entry (from, to) >= 0 of moves [B, Hkv, n, 2] int32, row `from`
     of sequence b and that K/V head (K, V, and pos and mass where given) goes to row `to`.  No row may be written twice,
     or written by one entry and read by another.  Returns (K_pool, V_pool)."""
-    n_pages, page, Hkv, d, k_page = _need_pool(K_pool, "K_pool")
-    v_page = _need_pool(V_pool, "V_pool", K_pool.shape)[4]
+    n_pages, page, Hkv, d, k_page, v_page = _need_pools(K_pool, V_pool)
     if table.dim() != 2:
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
     B, max_pages = table.shape
-    _need_exact(table, torch.int32, "table", (B, max_pages))
+    _need(table, torch.int32, "table")
     if moves.dim() != 4:
         raise ValueError(f"moves has shape {tuple(moves.shape)}, expected [{B}, {Hkv}, n, 2]")
     n = moves.shape[2]
     _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
-    if pos is not None:
-        _need_exact(pos, torch.int32, "pos", (n_pages, page, Hkv))
-    if mass is not None:
-        _need_exact(mass, torch.float32, "mass", (n_pages, page, Hkv))
+    _need_slots(pos, mass, (n_pages, page, Hkv))
     _, raw = _device_and_stream(stream, moves, table, K_pool, V_pool, pos, mass)
     st = lib().mla_cache_move(moves.data_ptr(), table.data_ptr(), K_pool.data_ptr(), V_pool.data_ptr(), k_page, v_page,
                               _addr(pos), _addr(mass), B, n, n_pages, page, max_pages, Hkv, d, raw)
