@@ -81,7 +81,7 @@ struct __align__(8) Barriers {
   uint64_t q_full, q_empty;
   uint64_t full[kSlots], empty[kSlots];
   uint64_t s_full[2], p_ready[2];
-  uint64_t pv_done;
+  uint64_t pv_done, o_full;  // a tile's PV, a piece's last PV
   uint64_t v_tail[2];  // alternating: a piece's tail may land while the piece before waits for its own
 };
 
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.p_ready[s], Sh::kReady);  // the worker's softmax warps
     }
     mbar_init(&bar.pv_done, 1);
+    mbar_init(&bar.o_full, 1);
     for (int s = 0; s < 2; ++s) mbar_init(&bar.v_tail[s], 1);
     abort_flag = 0;
     fence_mbarrier_init();
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             commit<kPair>(&bar.pv_done);
+            if (step == J) commit<kPair>(&bar.o_full);
           }
         }
         g += J;
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_lanes = tmem + (static_cast<uint32_t>(lane0) << 16);
     const int tid = threadIdx.x - 128;
     const uint32_t ready0 = cluster_addr(&bar.p_ready[0], 0);
-    uint32_t g = 0, u = 0, tails = 0;
+    uint32_t g = 0, u = 0, tails = 0, pieces = 0;
     bool ok = true;
     int head_flag = 0, tail_flag = 0, tail_tok = 0, tail_n = 0, tail_h = 0;  // for ws_meta
     for (Pieces w(p, start); !w.done(); w.next()) {
@@ -618,11 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       u += 2 * J * Sh::kParts;
-      // ---- output of the piece, once its last PV is done.  The last tile's scores only showed that
-      // the PV two tiles before it was: the one in between is waited for first, or its parity would
-      // be taken for the last one's.
-      if (g >= 2) ok = mbar_wait(&bar.pv_done, g & 1, &abort_flag, p.s.err) && ok;
-      ok = mbar_wait(&bar.pv_done, (g - 1) & 1, &abort_flag, p.s.err) && ok;
+      // ---- output of the piece, once its last PV is done.  (Not on pv_done: a phase of a barrier may only
+      // be waited for by its parity if the one before it is known to be complete.)
+      ok = mbar_wait(&bar.o_full, pieces & 1, &abort_flag, p.s.err) && ok;
+      ++pieces;
       tc_fence_after();
       const bool whole = w.j0 == 0 && w.j1 == w.n_keys;
       if (warp_valid) {
