@@ -349,8 +349,8 @@ hcadsa_status attn_gate_vha_fwd(const hcadsa_bf16* O, const hcadsa_bf16* cq, con
  *              evicted); NULL: kv_len
  *   pos, mass : [n_pages, page, Hkv] int32 / fp32, position and accumulated attention weight of every
  *              pool row
- * page is a power of two, 16 to 1024; d == 256; Hq / Hkv a power of two up to 128 (HCADSA_ERR_
- * UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and mass need 4-byte alignment (moves: 8),
+ * page is a power of two, 16 to 1024; d == 256; Hq / Hkv a power of two up to 128; the attention calls
+ * take up to 2^23 new tokens (HCADSA_ERR_UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and mass need 4-byte alignment (moves: 8),
  * the bf16 tensors 16.  The lengths and tables are device data: a value out of range (a page that
  * is not in the pool, a length beyond max_pages * page, cu_q out of order) is recorded as
  * HCADSA_ERR_DEVICE_BOUNDS, and the rows it concerns are skipped or read as zeros; nothing outside
@@ -378,9 +378,11 @@ hcadsa_status mla_cache_append(const hcadsa_bf16* K, const hcadsa_bf16* V, long 
  *     O[t,h] = sum_s softmax_s(scale <Q[t,h], K[s]>) V[s],   lse[t,h] = log sum_s exp(scale <Q[t,h], K[s]>)
  * Query head h reads K/V head h / (Hq/Hkv).  A token that sees no row (kv_len[b] < n_b) gets O = 0,
  * lse = -inf.  What lies in a page behind the last row of its sequence does not matter (NaN
- * included).
+ * included); the rows of the sequence itself should be finite, since a NaN or infinity in V also
+ * reaches the tokens that do not see its row but share a tile of 128 rows with it.
  *   Q   : [T, Hq, 256] bf16, tokens q_row_stride elements apart (a multiple of 8)
- *   O   : [T, Hq, 256] bf16 (written for the tokens of the batch); lse: [T, Hq] fp32 or NULL
+ *   O   : [T, Hq, 256] bf16 (written for the tokens of the batch; not over an input); lse: [T, Hq]
+ *         fp32 or NULL
  *   workspace : mla_paged_attn_fwd_workspace_size(...) bytes, 32-byte aligned, scratch: calls that
  *               share it must be serialised.  The size depends on the current device's SM count.
  * scale > 0 (HCADSA_ERR_SHAPE otherwise).  Results do not depend on timing.

@@ -136,6 +136,11 @@ CASES = {
     "decode_gqa": dict(q_len=[1, 1, 1], kv_len=[300, 64, 511], Hq=32, Hkv=4, page=32),
     "decode_mha": dict(q_len=[1, 1], kv_len=[255, 257], Hq=16, Hkv=16, page=128),
     "decode_group128": dict(q_len=[1, 2], kv_len=[130, 259], Hq=128, Hkv=1, page=64),
+    "decode_group128_one_token_each": dict(q_len=[1, 1, 1], kv_len=[130, 2000, 64], Hq=128, Hkv=1, page=32),
+    "decode_two_groups_of_128": dict(q_len=[1, 1], kv_len=[700, 129], Hq=256, Hkv=2, page=16),
+    "one_row_per_token": dict(q_len=[1] * 3, kv_len=[77, 400, 1000], Hq=3, Hkv=3, page=16),
+    "long_chunk": dict(q_len=[1100], kv_len=[2300], page=128),
+    "short_tail_tiles": dict(q_len=[5, 5, 5, 5], kv_len=[129, 257, 145, 17], page=16, Hq=32),
     "prompt_from_nothing": dict(q_len=[300], kv_len=[300]),
     "chunk_odd": dict(q_len=[37, 129], kv_len=[700, 129], page=16),
     "chunk_gqa_fused_pool": dict(q_len=[65, 1, 200], kv_len=[400, 33, 777], Hq=8, Hkv=2, page=256, interleaved=True),
@@ -440,6 +445,83 @@ def test_other_stream_and_graph(hd):
     want2, wl2 = hd.mla_paged_attn_fwd(c2.q, *c2.args(), return_lse=True)
     assert torch.equal(gO, want2) and torch.equal(gl, wl2)
     assert torch.equal(gm, hd.mla_paged_attn_mass(c2.q, c2.K, c2.table, c2.cu, c2.kv_len, wl2))
+    hd.hcadsa_check_device_error()
+
+
+def test_unaligned_outputs_and_workspaces(hd):
+    """O on a 16-byte boundary only, pos and mass on a 4-byte one, a caller's workspace, and the refusals of short or
+    misaligned ones."""
+    c = Cache([3, 70], [500, 140], seed=17, Hq=16)
+    want, wl = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+    buf = torch.zeros(73 * 16 * D + 8, dtype=bf, device="cuda")
+    O = buf[8:].view(73, 16, D)
+    need = hd.lib().mla_paged_attn_fwd_workspace_size(2, 73, 16, 1)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    hd.mla_paged_attn_fwd(c.q, *c.args(), O=O, workspace=ws[:need])
+    assert torch.equal(O, want) and (buf[:8] == 0).all()
+    for bad, what in ((ws[: need - 1], "WORKSPACE"), (ws[16:], "ALIGN")):
+        with pytest.raises(hd.HcaDsaError, match=what):
+            hd.mla_paged_attn_fwd(c.q, *c.args(), workspace=bad)
+    need = hd.lib().mla_paged_attn_mass_workspace_size(2, 73, 16, 1)
+    with pytest.raises(hd.HcaDsaError, match="WORKSPACE"):
+        hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, wl, workspace=ws[: need - 1])
+    mass = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, wl, workspace=ws[:need])
+    pos = torch.arange(mass.numel(), dtype=i32, device="cuda").view(mass.shape)
+    a, _ = hd.mla_evict_select(mass, pos, c.table, c.kv_len, None, 100, n_sink=2, n_recent=5)
+    off = [torch.cat([x.new_zeros(1), x.flatten()])[1:].view(x.shape) for x in (mass, pos)]
+    b, _ = hd.mla_evict_select(*off, c.table, c.kv_len, None, 100, n_sink=2, n_recent=5)
+    assert torch.equal(a, b)
+    hd.hcadsa_check_device_error()
+
+
+def test_two_calls_at_once(hd):
+    """Calls on two streams that overlap, each with its own outputs and workspace."""
+    cs = [Cache([1] * 6, [3000, 50, 777, 4096, 1, 129], seed=31), Cache([260, 1], [900, 2000], seed=32, page=16)]
+    want = []
+    for c in cs:
+        O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+        want.append((O, lse, hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True, stream=s)
+            got[i].append((O, lse, hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse, stream=s)))
+    torch.cuda.synchronize()
+    hd.hcadsa_check_device_error()
+    for w, many in zip(want, got):
+        for g in many:
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+def test_shared_pages(hd):
+    """Two sequences that share their first pages: attention reads them for both, and a shared row's mass is the sum."""
+    c = Cache([1, 20], [200, 200], seed=41, page=16)
+    c.table[1, :8] = c.table[0, :8]
+    at = c.rows(1)
+    c.K[at[0][128:], at[1][128:]] = c.rand(72, 1, D)
+    O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+    ref = oracle(c, lse_in=lse)
+    check_attn(c, O, lse, ref, "shared pages")
+    mass = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse)
+    assert ((mass.double() - ref[4]).abs() <= ref[5] + 2.0 ** -22 * ref[4]).all()
+    hd.hcadsa_check_device_error()
+
+
+def test_many_empty_sequences(hd):
+    """More sequences than threads in a block, most of them without tokens or rows."""
+    n = 1500
+    q = [3 if b % 401 == 7 else 0 for b in range(n)]
+    kv = [130 if q[b] else (b % 5) * 3 for b in range(n)]
+    c = Cache(q, kv, Hq=16, page=16, seed=43, width=9)
+    O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+    ref = oracle(c, lse_in=lse)
+    check_attn(c, O, lse, ref, "many")
+    mass = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse)
+    assert ((mass.double() - ref[4]).abs() <= ref[5] + 2.0 ** -23 * ref[4]).all()
+    none = hd.mla_paged_attn_fwd(c.q, c.K, c.V, c.table, torch.zeros_like(c.cu), c.kv_len, O=torch.ones_like(O))
+    assert (none == 1).all()
     hd.hcadsa_check_device_error()
 
 

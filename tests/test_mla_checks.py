@@ -70,6 +70,7 @@ def test_query_refusals(lib):
         assert call(qr=16383) == -2 and call(qr=16388) == -3
         assert call(scale=0.0) == -2 and call(scale=-1.0) == -2 and call(scale=float("nan")) == -2
         assert call(T=-1) == -2 and call(T=0) == 0
+        assert call(T=(1 << 23) + 1) == -4
     for bad in ((-1, 4, 64, 1), (2, 4, 48, 1), (2, 4, 7, 2), (0, 4, 64, 1), (2, 0, 64, 1), (2, 4, 0, 1), (2, 4, 64, 0)):
         assert lib.mla_paged_attn_fwd_workspace_size(*bad) == 0
         assert lib.mla_paged_attn_mass_workspace_size(*bad) == 0
