@@ -11,19 +11,27 @@
 // key tiles: CTA r holds rows 128 r .. 128 r + 127 (its TMEM lanes), and loads half of every K and
 // V tile -- K rows 64 r .. +63, V columns 128 r .. +127 -- which the pair's MMAs (cta_group::2,
 // M = 256) read from both.  One CTA alone (M = 128) would need 64 bytes of K and V per SM cycle at
-// the full MMA rate, the limit of the L2; the pair needs 32.
+// the full MMA rate, the limit of the L2; the pair needs 32.  Batches of short chunks (decode steps)
+// run on single CTAs with row tiles of 128 rows instead: see use_pairs.
 //   S  = Q (A, smem) * K^T (B, smem, K-major)        128 columns of TMEM, two buffers
 //   O += P (A, TMEM, bf16 over its own S) * V (B, smem, MN-major)   256 columns of TMEM
 // S and O together are all 512 columns.  Roles per CTA: warp 0 TMA (both CTAs; the lanes issue a
 // tile's page boxes side by side), warp 1 the MMA thread (leader CTA), warps 4-11 softmax, two
-// threads per row.  The reference maximum moves only when it is exceeded by 2^8 (lazy rescale of O).
+// threads per row.  The reference maximum moves only when it is exceeded by 2^8 (lazy rescale of
+// O).  P is rounded to bf16, the type the tensor cores take, after its sum was taken in fp32.
 //
 // Schedule: the (row tile, key tile) products of the whole batch form one list -- sequence, K/V
-// head, row tile, key tile -- whose length follows in closed form from the lengths.  Pair c of G
+// head, row tile, key tile -- whose length follows in closed form from the lengths.  Worker c of G
 // takes the products [c N / G, (c+1) N / G): equal work for prompts, chunks and single tokens alike,
-// decided on the device (the host never sees the lengths).  A row tile that several pairs share
+// decided on the device (the host never sees the lengths).  A row tile that several workers share
 // leaves unnormalised fp32 rows and (max, sum) in the workspace -- at most two such pieces per
-// pair -- and combine_kernel merges them in list order: the result does not depend on timing.
+// worker -- and combine_kernel merges them in list order: the result does not depend on timing.
+//
+// Measured (B200, 64 heads on one K/V head): 2048 tokens over 32768 rows 2.66 ms in a short run
+// (1.60 PFLOP/s), 3.01 ms when repeated (1.42 PFLOP/s; the power limit holds the clock at 1.43 GHz).
+// A product takes 2490 cycles of 2048 for its MMAs: the S MMAs read A and B from shared memory at
+// 128 bytes per cycle, its limit, next to the incoming tiles.  32 sequences of 1K-32K rows, one token
+// each: 105 us on the device, 5.4 TB/s.
 //
 // Rows behind the end of a sequence in its last page may hold anything.  Their scores are replaced
 // before the softmax, and since 0 * NaN is NaN, the V rows of such a tile are cleared in shared
@@ -816,7 +824,10 @@ size_t workspace_bytes_of(int sms) {
 
 // Pairs take row tiles of 256 rows and load half the K and V per product; single CTAs take row tiles
 // of 128 rows, so a sequence that has no more rows than that (a decode step) costs half the MMA time.
-// Both give right results for every batch; the host only knows the averages.
+// Both give right results for every batch; the host only knows the averages.  Measured, pairs and
+// single CTAs: 32 decode steps over 1K-32K rows 117 and 105 us; two 389-token chunks next to 22
+// decode steps (266 rows per sequence on average) 210 and 233 us; 2048 tokens over 32768 rows 3.0 and
+// 3.6 ms.
 bool use_pairs(int B, int T, int g) { return (long long)T * g > (long long)kCtaRows * B; }
 
 template <bool kPair>

@@ -22,6 +22,7 @@
 // What bounds it is latency: two dependent loads per row, three passes over the keys, four cluster
 // barriers.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
 // do not fit in shared memory are read from global memory again in every pass.
+// Measured (B200): 32 lists of 4224 rows cut to 4096 in 12.4 us, 4 lists of 131072 cut to 32768 in 27.
 #include <mutex>
 
 #include "mla_host.h"

@@ -6,20 +6,25 @@
 //                of exp(scale <q[t], k_s> - lse[t])
 // with the log-sum-exp of the attention call.
 //
-// Tiles: keys are the M of the products.  A CTA pair holds 256 cache rows (CTA r the rows 128 r ..
-// +127, its TMEM lanes) and streams the chunk's (token, head) rows past them, 128 per tile (64 loaded
-// by each CTA): S^T = K (A) * Q^T (B), tcgen05 cta_group::2, M = 256, N = 128.  A thread owns a cache
-// row and sums exp2 over its TMEM lane's 128 columns: the sum over tokens and heads needs no exchange
-// between threads and no atomics.  Four S buffers (all of TMEM) decouple the MMAs from the sums; two
-// warpgroups take the tiles in turn.  The exponentials bound it: 128 x 128 of them per CTA and tile
-// take 1024 cycles on the SFUs, exactly what the MMAs take.
+// Tiles: keys are the M of the products.  A CTA pair holds a block of 256 cache rows (CTA r the rows
+// 128 r .. +127, its TMEM lanes) and streams the chunk's (token, head) rows past them, 128 per tile
+// (64 loaded by each CTA): S^T = K (A) * Q^T (B), tcgen05 cta_group::2, M = 256, N = 128.  A thread
+// owns a cache row and sums exp2 over its TMEM lane's 128 columns, so the sum over tokens and heads
+// needs no exchange between threads, but one at the end of a block, and no atomics.  Four S buffers
+// (all of TMEM), one warpgroup for each: a TMEM load takes about 600 cycles next to the MMAs, and
+// four warps per scheduler hide it.  The sums are fp32, over the tiles with Kahan's compensation.
 // A decode step has few rows per sequence: the same Q tile stays in its slot from one block of cache
-// rows to the next, and the kernel streams K at HBM rate.
+// rows to the next, and the kernel streams K.
 //
 // Schedule: as the attention kernel's, one list of (256-row block, 128-row Q tile) products over the
 // batch -- sequence, K/V head, block, Q tile, those that see some row of the block -- cut evenly over
 // the pairs.  A block that several pairs share leaves partial sums in the workspace, which
 // add_kernel adds up in list order; every row's mass gets exactly one addition per call.
+//
+// Measured (B200, 64 heads on one K/V head): 1021 tokens over 16381 rows 397 us in a short run (1.34
+// PFLOP/s), 465 us when repeated (power limit); the MMAs and loads alone, without the sums, take 313.
+// Products of 256 columns (two S buffers) took 412 us, K held in TMEM as the A operand 417.  A decode
+// step of 32 sequences of 1K-32K rows: 55 us for the kernel (5.2 TB/s), 61 with zeroing and adding up.
 #include <mutex>
 
 #include "mla_host.h"
