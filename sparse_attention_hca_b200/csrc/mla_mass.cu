@@ -317,36 +317,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc = idesc_bf16_f32(kKeys, kCols, false, false);
+    // ------------------------------------------------------------ MMA issuer (leader CTA)
+    // The whole warp walks and waits, one elected lane issues: the descriptors stay warp-uniform values.
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(kKeys, kCols, false, false);
       const uint32_t sKa = smem_u32(sK), sQa = smem_u32(sQ);
+      auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, &abort_flag, p.s.err));
+      };
       uint32_t piece = 0, u = 0, n = 0;  // n: products so far (S buffer n & 3)
       bool ok = true;
       for (Walk w(p, start); !w.done() && ok; w.next(), ++piece) {
         const uint32_t kb = piece & 1;
-        ok = mbar_wait(&bar.k_full[kb], (piece >> 1) & 1, &abort_flag, p.s.err);
+        ok = wait(&bar.k_full[kb], (piece >> 1) & 1);
         const uint64_t da = smem_desc_sw128(sKa + kb * kKBytes, 16, 1024);
         for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
           const uint32_t s = u % kQSlots, sb = n & 3;
-          ok = mbar_wait(&bar.q_full[s], (u / kQSlots) & 1, &abort_flag, p.s.err) &&
-               mbar_wait(&bar.s_empty[sb], ((n >> 2) & 1) ^ 1, &abort_flag, p.s.err);
+          const bool last = t + 1 == w.t1, keep = last && w.same_tile_next();
+          ok = wait(&bar.q_full[s], (u / kQSlots) & 1) && wait(&bar.s_empty[sb], ((n >> 2) & 1) ^ 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t db = smem_desc_sw128(sQa + s * kQBytes, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
-              mma_ss_pair(tmem + sb * kCols, da + (uint64_t)((c * kKChunk + kk * 32) >> 4),
-                          db + (uint64_t)((c * kQChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
-          mma_commit_pair(&bar.s_full[sb]);
-          const bool last = t + 1 == w.t1;
-          if (!(last && w.same_tile_next())) {
-            mma_commit_pair(&bar.q_empty[s]);
-            ++u;
+              for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
+                mma_ss_pair(tmem + sb * kCols, da + (uint64_t)((c * kKChunk + kk * 32) >> 4),
+                            db + (uint64_t)((c * kQChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
+            mma_commit_pair(&bar.s_full[sb]);
+            if (!keep) mma_commit_pair(&bar.q_empty[s]);
+            if (last) mma_commit_pair(&bar.k_empty[kb]);
           }
-          if (last) mma_commit_pair(&bar.k_empty[kb]);
+          __syncwarp();
+          if (!keep) ++u;
         }
       }
     }
