@@ -443,71 +443,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader)
-    if (lane == 0 && rank == 0) {
-      const uint32_t idesc_s = idesc_bf16_f32(Sh::kRows, kKeyTile, false, false);
-      const uint32_t idesc_o = idesc_bf16_f32(Sh::kRows, kMlaD, false, true);
-      const uint32_t sQa = smem_u32(sQ), sRa = smem_u32(sRing);
-      const uint64_t dq = smem_desc_sw128(sQa, 16, 1024);
+    // ------------------------------------------------------------ MMA issuer (leader CTA)
+    // The whole warp walks and waits, one elected lane issues: the descriptors stay warp-uniform values.
+    if (rank == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(Sh::kRows, kKeyTile, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(Sh::kRows, kMlaD, false, true);
+      const uint32_t sRa = smem_u32(sRing);
+      const uint64_t dq = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+      auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(b, parity, &abort_flag, p.s.err));
+      };
       uint32_t u = 0, it = 0, g = 0;  // g: key tiles so far (S buffer and barrier phases)
       bool ok = true;
       for (Pieces w(p, start); !w.done() && ok; w.next(), ++it) {
         const int J = w.tiles();
-        ok = mbar_wait(&bar.q_full, it & 1, &abort_flag, p.s.err);
+        ok = wait(&bar.q_full, it & 1);
         for (int step = 0; step <= J && ok; ++step) {
           if (step < J) {
             const uint32_t gs = g + step, tS = tmem + kTmemS + (gs & 1) * kKeyTile;
 #pragma unroll
             for (int part = 0; part < Sh::kParts && ok; ++part) {
               const uint32_t s = u % kSlots;
-              ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+              ok = wait(&bar.full[s], (u / kSlots) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, 1024);
+              if (elect_one()) {
 #pragma unroll
-              for (int c = 0; c < 4 / Sh::kParts; ++c)
+                for (int c = 0; c < 4 / Sh::kParts; ++c)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {  // start addresses in 16-byte units
-                  const uint64_t a = dq + (uint64_t)(((part * 2 + c) * kQChunk + kk * 32) >> 4);
-                  const uint64_t b = dk + (uint64_t)((c * Sh::kKChunk + kk * 32) >> 4);
-                  if constexpr (kPair) mma_ss_pair(tS, a, b, idesc_s, (part | c | kk) != 0);
-                  else mma_ss(tS, a, b, idesc_s, (part | c | kk) != 0);
+                  for (int kk = 0; kk < 4; ++kk) {  // start addresses in 16-byte units
+                    const uint64_t a = dq + (uint64_t)(((part * 2 + c) * kQChunk + kk * 32) >> 4);
+                    const uint64_t b = dk + (uint64_t)((c * Sh::kKChunk + kk * 32) >> 4);
+                    if constexpr (kPair) mma_ss_pair(tS, a, b, idesc_s, (part | c | kk) != 0);
+                    else mma_ss(tS, a, b, idesc_s, (part | c | kk) != 0);
+                  }
+                commit<kPair>(&bar.empty[s]);
+                if (part == Sh::kParts - 1) {
+                  commit<kPair>(&bar.s_full[gs & 1]);
+                  if (step == J - 1) commit<kPair>(&bar.q_empty);
                 }
-              commit<kPair>(&bar.empty[s]);
+              }
+              __syncwarp();
               ++u;
             }
-            if (!ok) break;
-            commit<kPair>(&bar.s_full[gs & 1]);
-            if (step == J - 1) commit<kPair>(&bar.q_empty);
           }
-          if (step >= 1) {
+          if (step >= 1 && ok) {
             const uint32_t gj = g + step - 1;
             const uint32_t tP = tmem + kTmemS + (gj & 1) * kKeyTile;  // bf16 pairs: 64 columns
 #pragma unroll
             for (int part = 0; part < Sh::kParts && ok; ++part) {
               const uint32_t s = u % kSlots;
-              ok = mbar_wait(&bar.full[s], (u / kSlots) & 1, &abort_flag, p.s.err);
+              ok = wait(&bar.full[s], (u / kSlots) & 1);
               if (ok && part == 0)
                 ok = kPair && is_tail(w.q.len, w.j0 + step - 1)
-                         ? mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err)
-                         : mbar_wait(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err);
+                         ? __all_sync(0xffffffffu,
+                                      mbar_wait_cluster(&bar.p_ready[gj & 1], (gj >> 1) & 1, &abort_flag, p.s.err))
+                         : wait(&bar.p_ready[gj & 1], (gj >> 1) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, Sh::kVChunk, 1024);
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kKeyTile / 16 / Sh::kParts; ++kk) {
-                const uint32_t a = tP + (part * 4 + kk) * 8;
-                const uint64_t b = dv + (uint64_t)((kk * 2048) >> 4);
-                const uint32_t acc = (step > 1 || part > 0 || kk > 0) ? 1u : 0u;
-                if constexpr (kPair) mma_ts_pair(tmem, a, b, idesc_o, acc);
-                else mma_ts(tmem, a, b, idesc_o, acc);
+                for (int kk = 0; kk < kKeyTile / 16 / Sh::kParts; ++kk) {
+                  const uint32_t a = tP + (part * 4 + kk) * 8;
+                  const uint64_t b = dv + (uint64_t)((kk * 2048) >> 4);
+                  const uint32_t acc = (step > 1 || part > 0 || kk > 0) ? 1u : 0u;
+                  if constexpr (kPair) mma_ts_pair(tmem, a, b, idesc_o, acc);
+                  else mma_ts(tmem, a, b, idesc_o, acc);
+                }
+                commit<kPair>(&bar.empty[s]);
+                if (part == Sh::kParts - 1) {
+                  commit<kPair>(&bar.pv_done);
+                  if (step == J) commit<kPair>(&bar.o_full);
+                }
               }
-              commit<kPair>(&bar.empty[s]);
+              __syncwarp();
               ++u;
             }
-            if (!ok) break;
-            commit<kPair>(&bar.pv_done);
-            if (step == J) commit<kPair>(&bar.o_full);
           }
         }
         g += J;
