@@ -733,79 +733,169 @@ __global__ void __launch_bounds__(kThreads, 1)
 // c+1, c+2, ... (piece k >= 1 is the one worker c + k began with), in that order: with M the largest
 // of the maxima,
 //     O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
-// One warp per row; the lanes read the pieces' (max, sum) side by side, so the loads of the rows
-// themselves (lane l: columns 8 l .. 8 l + 7) do not wait on one another.
+// Every block lists the row tiles to merge from the workers' records and takes its share of the work
+// items: with up to kFewPieces pieces an item is 8 rows, one warp each; with more (a long cache cut
+// over many workers) it is one row, whose pieces the 8 warps divide among themselves and add up
+// through shared memory, in warp order.  Lane l holds columns 8 l .. 8 l + 7; the lanes read the
+// pieces' (max, sum) side by side, so the loads of the rows do not wait on one another.
+// (One sequence of 32768 rows, 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
 constexpr int kCombineWarps = 8;
+constexpr int kFewPieces = 8;
 constexpr int kMaxWorkers = 160;
 
-__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p, int n_workers, int n_rows) {
+// Columns 8 l .. 8 l + 7 of piece k's row, added to acc with weight w.
+__device__ __forceinline__ void add_piece(const float4& a, const float4& b, float w, float (&acc)[8]) {
+  if (w > 0.0f) {  // a piece without weight may hold anything
+    acc[0] = fmaf(w, a.x, acc[0]);
+    acc[1] = fmaf(w, a.y, acc[1]);
+    acc[2] = fmaf(w, a.z, acc[2]);
+    acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]);
+    acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]);
+    acc[7] = fmaf(w, b.w, acc[7]);
+  }
+}
+
+__global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Params p, int n_workers, int n_rows) {
+  __shared__ int pieces_of[kMaxWorkers], first_item[kMaxWorkers + 1];
+  __shared__ int4 tile_of[kMaxWorkers];  // first packed token, tokens, K/V head
+  __shared__ uint32_t ends[kMaxWorkers / 32];  // bit c: worker c's first piece, if any, is the last of its row tile
+  __shared__ float weight[kMaxWorkers], red[2][kCombineWarps], part[kCombineWarps][kMlaD];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_for_primary();
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  const int* meta = p.ws_meta + c * kMetaInts;
-  if (!meta[1]) return;
-  const int tok = row >> p.g_log2;
-  if (tok >= meta[3]) return;
-  int n = 1;  // pieces
-  for (int k0 = c + 1; k0 < n_workers; k0 += 32) {
-    const int flag = k0 + lane < n_workers ? p.ws_meta[(k0 + lane) * kMetaInts] : 2;
-    const uint32_t last = __ballot_sync(0xffffffffu, flag != 1);
-    if (last) {
-      n += __ffs(last);
-      break;
-    }
-    n += 32;
-  }
-  n = min(n, n_workers - c);
-  float m[kMaxWorkers / 32], l[kMaxWorkers / 32], M = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < kMaxWorkers / 32; ++q) {
-    const int k = q * 32 + lane;
-    m[q] = -INFINITY;
-    l[q] = 0.0f;
-    if (k < n) {
-      const float* ml = p.ws_ml + (size_t)(k ? 2 * (c + k) : 2 * c + 1) * 2 * n_rows + row;
-      m[q] = ml[0];
-      l[q] = ml[n_rows];
-    }
-    if (l[q] > 0.0f) M = fmaxf(M, m[q]);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float den = 0.0f, acc[8] = {};
-#pragma unroll
-  for (int q = 0; q < kMaxWorkers / 32; ++q) {
-    const float w_mine = l[q] > 0.0f ? exp2f(m[q] - M) : 0.0f;
-    const int n_q = min(32, n - q * 32);
-#pragma unroll 4
-    for (int k = 0; k < n_q; ++k) {
-      const float w = __shfl_sync(0xffffffffu, w_mine, k), lk = __shfl_sync(0xffffffffu, l[q], k);
-      const int piece = q * 32 + k;
-      const float4* src = reinterpret_cast<const float4*>(
-          p.ws_O + ((size_t)(piece ? 2 * (c + piece) : 2 * c + 1) * n_rows + row) * kMlaD + lane * 8);
-      const float4 a = src[0], b = src[1];
-      if (w > 0.0f) {
-        den = fmaf(w, lk, den);
-        acc[0] = fmaf(w, a.x, acc[0]);
-        acc[1] = fmaf(w, a.y, acc[1]);
-        acc[2] = fmaf(w, a.z, acc[2]);
-        acc[3] = fmaf(w, a.w, acc[3]);
-        acc[4] = fmaf(w, b.x, acc[4]);
-        acc[5] = fmaf(w, b.y, acc[5]);
-        acc[6] = fmaf(w, b.z, acc[6]);
-        acc[7] = fmaf(w, b.w, acc[7]);
+  // ---- row tiles to merge: their pieces and work items, and the prefix of the items
+  const int* mine = p.ws_meta + tid * kMetaInts;
+  const int head = tid < n_workers ? mine[0] : 2, tail = tid < n_workers ? mine[1] : 0;
+  const int rows = tail ? mine[3] << p.g_log2 : 0;
+  const uint32_t end_bits = __ballot_sync(0xffffffffu, head != 1);
+  if (lane == 0 && warp < kMaxWorkers / 32) ends[warp] = end_bits;
+  __syncthreads();
+  if (tid < kMaxWorkers) {
+    int items = 0;
+    if (tail) {
+      int c = tid + 1;  // the first worker from here on whose first piece ends the tile
+      while (c < n_workers) {
+        const uint32_t left = ends[c >> 5] >> (c & 31);
+        if (left) {
+          c += __ffs(left) - 1;
+          break;
+        }
+        c = (c | 31) + 1;
       }
+      const int n = min(c, n_workers - 1) - tid + 1;
+      pieces_of[tid] = n;
+      tile_of[tid] = make_int4(mine[2], mine[3], mine[4], 0);
+      items = n <= kFewPieces ? (rows + kCombineWarps - 1) / kCombineWarps : rows;
+    }
+    first_item[tid + 1] = items;
+    if (tid == 0) first_item[0] = 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int run = 0;
+#pragma unroll
+    for (int w0 = 0; w0 < kMaxWorkers; w0 += 32) {
+      int x = first_item[w0 + lane + 1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      first_item[w0 + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-  const size_t orow = (size_t)(meta[2] + tok) * p.Hq + (meta[4] << p.g_log2) + (row & ((1 << p.g_log2) - 1));
-  uint4 v;
-  v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-  v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
-  v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
-  reinterpret_cast<uint4*>(p.O + orow * kMlaD)[lane] = v;
-  if (p.lse && lane == 0) p.lse[orow] = den > 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
+  __syncthreads();
+  const int total = first_item[kMaxWorkers];
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int c = 0, hi = kMaxWorkers;  // the last worker whose items begin at or before this one
+    while (hi - c > 1) {
+      const int mid = (c + hi) >> 1;
+      if (first_item[mid] <= item) c = mid;
+      else hi = mid;
+    }
+    const int4 tile = tile_of[c];
+    const int n = pieces_of[c];
+    const bool few = n <= kFewPieces;
+    const int row = few ? (item - first_item[c]) * kCombineWarps + warp : item - first_item[c];
+    const int tok = row >> p.g_log2;
+    auto slot = [&](int k) { return (size_t)(k ? 2 * (c + k) : 2 * c + 1); };
+    auto row_of = [&](int k) {
+      return reinterpret_cast<const float4*>(p.ws_O + (slot(k) * n_rows + row) * kMlaD + lane * 8);
+    };
+    float M, den, acc[8] = {};
+    if (few) {
+      if (tok >= tile.y) continue;
+      float m = -INFINITY, l = 0.0f;
+      if (lane < n) {
+        const float* ml = p.ws_ml + slot(lane) * 2 * n_rows + row;
+        m = ml[0];
+        l = ml[n_rows];
+      }
+      M = l > 0.0f ? m : -INFINITY;
+#pragma unroll
+      for (int o = kFewPieces / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      M = __shfl_sync(0xffffffffu, M, 0);  // (the first kFewPieces lanes hold the pieces)
+      const float w_mine = l > 0.0f ? exp2f(m - M) : 0.0f;
+      den = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < n; ++k) {
+        const float w = __shfl_sync(0xffffffffu, w_mine, k), lk = __shfl_sync(0xffffffffu, l, k);
+        const float4 a = row_of(k)[0], b = row_of(k)[1];
+        den = fmaf(w, lk, den);
+        add_piece(a, b, w, acc);
+      }
+    } else {
+      // thread k: piece k's maximum and sum, then its weight
+      float m = -INFINITY, l = 0.0f;
+      if (tid < n) {
+        const float* ml = p.ws_ml + slot(tid) * 2 * n_rows + row;
+        m = ml[0];
+        l = ml[n_rows];
+      }
+      M = l > 0.0f ? m : -INFINITY;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      __syncthreads();  // the item before has been read
+      if (lane == 0) red[0][warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, red[0][w]);
+      const float w_mine = l > 0.0f ? exp2f(m - M) : 0.0f;
+      if (tid < n) weight[tid] = w_mine;
+      den = w_mine * l;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      if (lane == 0) red[1][warp] = den;
+      __syncthreads();
+#pragma unroll 8
+      for (int k = warp; k < n; k += kCombineWarps) {
+        const float4 a = row_of(k)[0], b = row_of(k)[1];
+        add_piece(a, b, weight[k], acc);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) part[warp][lane * 8 + x] = acc[x];
+      __syncthreads();
+      if (warp != 0) continue;
+      den = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kCombineWarps; ++w) den += red[1][w];
+#pragma unroll
+      for (int w = 1; w < kCombineWarps; ++w)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] += part[w][lane * 8 + x];
+    }
+    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+    const size_t orow = (size_t)(tile.x + tok) * p.Hq + (tile.z << p.g_log2) + (row & ((1 << p.g_log2) - 1));
+    uint4 v;
+    v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+    v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+    v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
+    reinterpret_cast<uint4*>(p.O + orow * kMlaD)[lane] = v;
+    if (p.lse && lane == 0) p.lse[orow] = den > 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 // SMs of the current device, its kernels' shared memory set up.
@@ -860,8 +950,7 @@ hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
-  return launch_after(combine_kernel, dim3(workers, Shape<kPair>::kRows / kCombineWarps), 32 * kCombineWarps, stream,
-                      p, workers, (int)Shape<kPair>::kRows);
+  return launch_after(combine_kernel, dim3(4 * sms), 32 * kCombineWarps, stream, p, workers, (int)Shape<kPair>::kRows);
 }
 
 }  // namespace
