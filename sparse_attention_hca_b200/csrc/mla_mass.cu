@@ -509,15 +509,20 @@ __global__ void __launch_bounds__(kKeys) add_kernel(const Params p, int n_worker
   const int c = blockIdx.x;
   const int* meta = p.ws_meta + c * kMetaInts;
   if (!meta[1]) return;
+  int n = 1;  // pieces: up to the one that ends the block (the lanes read the records side by side)
+  for (int k0 = c + 1; k0 < n_workers; k0 += 32) {
+    const int lane = threadIdx.x & 31;
+    const int flag = k0 + lane < n_workers ? p.ws_meta[(k0 + lane) * kMetaInts] : 2;
+    const uint32_t last = __ballot_sync(0xffffffffu, flag != 1);
+    n += last ? __ffs(last) : 32;
+    if (last) break;
+  }
+  n = min(n, n_workers - c);
   const int b = meta[2], h = meta[3], key = meta[4] * kKeys + threadIdx.x;
   if (key >= paged_len(p.s, b, false)) return;
   float sum = p.ws_sum[(size_t)(2 * c + 1) * kKeys + threadIdx.x];
-  for (int k = c + 1; k < n_workers; ++k) {
-    const int flag = p.ws_meta[k * kMetaInts];
-    if (!flag) break;
-    sum += p.ws_sum[(size_t)(2 * k) * kKeys + threadIdx.x];
-    if (flag == 2) break;
-  }
+#pragma unroll 8
+  for (int k = 1; k < n; ++k) sum += p.ws_sum[(size_t)(2 * (c + k)) * kKeys + threadIdx.x];
   const int pg = paged_page(p.s, b, key);
   if (pg < 0) return;
   const int in = key & ((1 << p.s.page_log2) - 1);
