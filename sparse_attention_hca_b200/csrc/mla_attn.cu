@@ -209,9 +209,30 @@ struct Walk {
   }
 };
 
+// Where a worker's share begins: product x of the list, or the start or end of the row tile that
+// holds it, whichever is nearer, if that tile is short: a cut costs its partial rows, written and
+// merged, about as much as 8 products, and moving it at most half the tile's length in balance.
+// Shares of one or two products are cut all the same: there the time is that of the longest one.
+// Nor are single CTAs' (a few rows a sequence) moved: their partial rows are few.
+// (256 tokens on 1024 rows, 64 heads: 27.1 us against 41.0; but 32 sequences of one token on up to
+// 4000 rows 36.3 against 33.1 when single CTAs did the same.)
+constexpr int kShortTile = 12;
+
+__device__ __forceinline__ long long snap(const SeqTiles& t, long long from, long long per_head, long long x,
+                                          long long share) {
+  if (t.base >= kShortTile * kKeyTile) return x;  // (every tile of the sequence is long)
+  const long long in = (x - from) % per_head;
+  const int i = t.find(in), n = t.key_tiles(i);
+  if (n > kShortTile || n > 2 * share) return x;
+  const long long j = in - t.before(i);
+  return x - j + (2 * j >= n ? n : 0);
+}
+
 // Every thread of the CTA: this worker's share of the list.
+template <bool kPair>
 __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int worker, int n_workers, Start* out) {
-  __shared__ long long sums[kThreads / 32 + 1];
+  __shared__ long long sums[kThreads / 32];
+  __shared__ long long cut[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto work_of = [&](int b, bool report) -> long long {
     if (b >= p.s.B) return 0;
@@ -238,30 +259,54 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   };
   long long mine = 0, all;
   for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
-  scan(mine, all);
+  const long long mine_to = scan(mine, all);
   // a short list goes to as many workers as it has products, so that consecutive pieces of a row
   // tile always lie with consecutive workers
   const int n = all < n_workers ? (int)all : n_workers;
-  const long long lo = worker < n ? all * worker / n : 0, hi = worker < n ? all * (worker + 1) / n : 0;
+  if (tid == 0) out->count = 0;
+  if (worker >= n) return;
+  const long long x0 = all * worker / n, x1 = all * (worker + 1) / n, share = all / n;
+  // f(sequence, its products [from, upto)) for every sequence, all threads side by side
+  auto each = [&](auto&& f) {
+    long long done = 0;
+    for (int b0 = 0; b0 < p.s.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      if (p.s.B <= kThreads) {  // known from the first pass
+        if (mine > 0) f(b, mine_to - mine, mine_to);
+      } else {
+        long long total;
+        const long long w = work_of(b, false), upto = done + scan(w, total);
+        if (w > 0) f(b, upto - w, upto);
+        done += total;
+      }
+    }
+  };
+  if (tid < 2) cut[tid] = tid ? x1 : x0;
+  __syncthreads();
+  if (kPair && share >= 3) {
+    each([&](int b, long long from, long long upto) {
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
+        const long long x = e ? x1 : x0;
+        if (from <= x && x < upto)
+          cut[e] = snap(seq_tiles(paged_seq(p.s, b, false), tq_log2), from, (upto - from) / p.Hkv, x, share);
+      }
+    });
+    __syncthreads();
+  }
+  const long long lo = cut[0], hi = cut[1];
   if (tid == 0) out->count = hi - lo;
-  long long done = 0;
-  for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
-    const long long w = p.s.B <= kThreads ? mine : work_of(b0 + tid, false);
-    long long total;
-    const long long upto = done + scan(w, total), from = upto - w;
+  each([&](int b, long long from, long long upto) {
     if (from <= lo && lo < upto) {
-      const SeqTiles t = seq_tiles(paged_seq(p.s, b0 + tid, false), tq_log2);
-      const long long per_head = w / p.Hkv, r = lo - from;
-      out->b = b0 + tid;
+      const SeqTiles t = seq_tiles(paged_seq(p.s, b, false), tq_log2);
+      const long long per_head = (upto - from) / p.Hkv, r = lo - from;
+      out->b = b;
       out->h = (int)(r / per_head);
       const long long in = r - out->h * per_head;
       out->i = t.find(in);
       out->j = (int)(in - t.before(out->i));
     }
-    done += total;
-    if (done > lo) break;
-  }
-  __syncthreads();
+  });
 }
 
 __device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
@@ -333,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  find_start(p, Sh::kRowsLog2 - p.g_log2, worker, n_workers, &start);
+  find_start<kPair>(p, Sh::kRowsLog2 - p.g_log2, worker, n_workers, &start);
   tc_fence_before();
   __syncthreads();
   if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
