@@ -152,6 +152,9 @@ CASES = {
     "fused_projection": dict(q_len=[50, 1], kv_len=[333, 200], Hq=16, Hkv=2, fused=True),
     "sharp": dict(q_len=[33, 1], kv_len=[500, 3000], sigma=8.0),
     "many_sequences": dict(q_len=[1, 2, 0, 3] * 120, kv_len=[40, 2, 5, 177] * 120, Hq=16, page=16),
+    "many_prompts": dict(q_len=[4, 0, 9, 1, 40] * 100, kv_len=[300, 10, 9, 150, 700] * 100, Hq=16, page=32),
+    "short_row_tiles": dict(q_len=[256], kv_len=[1024]),
+    "short_and_long_row_tiles": dict(q_len=[100, 64, 31], kv_len=[1200, 5000, 31], Hq=32, Hkv=2, page=128),
     "long_decode": dict(q_len=[1, 4], kv_len=[40000, 20001], page=64),
 }
 
