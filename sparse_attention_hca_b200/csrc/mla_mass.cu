@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kKeys = 256;                  // cache rows of a block (128 per CTA)
 constexpr int kCols = 128;                  // (token, head) rows of a Q tile (64 loaded per CTA)
-constexpr int kKBytes = 64 * 1024, kKChunk = 16 * 1024;
+constexpr int kKBytes = 64 * 1024;
 constexpr int kQSlots = 3, kQBytes = 32 * 1024, kQChunk = 8 * 1024;
 constexpr int kSmemBytes = 2 * kKBytes + kQSlots * kQBytes;
 constexpr int kGroups = 4;                  // warpgroups that sum, one per S buffer
@@ -49,7 +49,8 @@ struct Params {
   float* mass;
   float* ws_sum;  // [2 G][256]: pair c's block that began before its range (2 c) or in it (2 c + 1)
   int* ws_meta;   // [G][kMetaInts]
-  int Hq, Hkv, g_log2, box_log2;
+  int Hq, Hkv, g_log2;
+  int box_log2, k_group, k_chunk;  // K rows of a box; bytes from 8 rows to the next, from 64 columns to the next
   float scale_log2;
 };
 
@@ -277,8 +278,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (all lanes)
-    const int n_tma = 512 >> p.box_log2;  // boxes of 128 K rows: 128 / box rows x 4 chunks, one per lane
-    const int krow = (lane >> 2) << p.box_log2, kchunk = lane & 3;
+    // boxes of 128 K rows, one per lane: 8 rows x 4 chunks, or 128 / box rows x 1 chunk
+    const bool groups = p.box_log2 == 3;
+    const int krow = groups ? 8 * lane : (lane >> 2) << p.box_log2, kchunk = groups ? 0 : lane & 3;
+    const int kboxes = groups ? 16 : 512 >> p.box_log2, kdst = krow * (p.k_group >> 3) + kchunk * p.k_chunk;
     const int g64 = p.g_log2 < 6 ? p.g_log2 : 6;  // heads of a Q box; a group of 128 is two boxes, one per CTA
     uint32_t piece = 0, u = 0;                    // u: Q tiles loaded
     bool ok = true, loaded = false;
@@ -286,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t kb = piece & 1;
       const int row = w.k * kKeys + 128 * (int)rank + krow;
       int pg = p.s.n_pages;  // a page that is not there: zeros (outside the tensor map)
-      if (lane < n_tma && row < w.q.len) {
+      if (lane < kboxes && row < w.q.len) {
         pg = paged_page(p.s, w.b, row);
         if (pg < 0) pg = p.s.n_pages;
       }
@@ -294,9 +297,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.k_full[kb], 2 * kKBytes);
       __syncwarp();
-      if (lane < n_tma)
-        tma_load_4d_pair(sK + kb * kKBytes + kchunk * kKChunk + krow * 128, &map_k, cluster_addr(&bar.k_full[kb], 0),
-                         kchunk * 64, w.h, row & page_mask, pg);
+      if (lane < kboxes)
+        tma_load_5d_pair(sK + kb * kKBytes + kdst, &map_k, cluster_addr(&bar.k_full[kb], 0), 0, row & page_mask,
+                         kchunk, w.h, pg);
       for (int t = w.t0; t < w.t1 && ok; ++t) {
         if (!loaded) {
           const uint32_t s = u % kQSlots;
@@ -330,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (Walk w(p, start); !w.done() && ok; w.next(), ++piece) {
         const uint32_t kb = piece & 1;
         ok = wait(&bar.k_full[kb], (piece >> 1) & 1);
-        const uint64_t da = smem_desc_sw128(sKa + kb * kKBytes, 16, 1024);
+        const uint64_t da = smem_desc_sw128(sKa + kb * kKBytes, 16, p.k_group);
         for (int t = w.t0; t < w.t1 && ok; ++t, ++n) {
           const uint32_t s = u % kQSlots, sb = n & 3;
           const bool last = t + 1 == w.t1, keep = last && w.same_tile_next();
@@ -343,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)  // start addresses in 16-byte units
-                mma_ss_pair(tmem + sb * kCols, da + (uint64_t)((c * kKChunk + kk * 32) >> 4),
+                mma_ss_pair(tmem + sb * kCols, da + (uint64_t)((c * p.k_chunk + kk * 32) >> 4),
                             db + (uint64_t)((c * kQChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
             mma_commit_pair(&bar.s_full[sb]);
             if (!keep) mma_commit_pair(&bar.q_empty[s]);
@@ -588,7 +591,10 @@ extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_r
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.g_log2 = log2_of(Hq / Hkv);
-  p.box_log2 = page < 64 ? log2_of(page) : 6;
+  const bool groups = page < 32;
+  p.box_log2 = groups ? 3 : page < 64 ? log2_of(page) : 6;
+  p.k_group = groups ? 4096 : 1024;
+  p.k_chunk = groups ? 1024 : kKBytes / 4;
   p.scale_log2 = scale * 1.4426950408889634f;
   CUtensorMap mq, mk;
   {
@@ -599,10 +605,10 @@ extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_r
     if (!encode_tmap_bf16(&mq, 3, const_cast<hcadsa_bf16*>(Q), dims, strides, box, true)) return HCADSA_ERR_CUDA;
   }
   {
-    const uint64_t dims[4] = {(uint64_t)kMlaD, (uint64_t)Hkv, (uint64_t)page, (uint64_t)n_pages};
-    const uint64_t strides[3] = {(uint64_t)kMlaD * 2, (uint64_t)Hkv * kMlaD * 2, (uint64_t)k_page_stride * 2};
-    const uint32_t box[4] = {64, 1, 1u << p.box_log2, 1};
-    if (!encode_tmap_bf16(&mk, 4, const_cast<hcadsa_bf16*>(K_pool), dims, strides, box, true)) return HCADSA_ERR_CUDA;
+    const uint64_t dims[5] = {64, (uint64_t)page, kMlaD / 64, (uint64_t)Hkv, (uint64_t)n_pages};
+    const uint64_t strides[4] = {(uint64_t)Hkv * kMlaD * 2, 64 * 2, (uint64_t)kMlaD * 2, (uint64_t)k_page_stride * 2};
+    const uint32_t box[5] = {64, 1u << p.box_log2, groups ? kMlaD / 64 : 1, 1, 1};
+    if (!encode_tmap_bf16(&mk, 5, const_cast<hcadsa_bf16*>(K_pool), dims, strides, box, true)) return HCADSA_ERR_CUDA;
   }
   mass_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, p);
   HCADSA_TRY(launch_status());
