@@ -58,6 +58,12 @@ constexpr uint32_t kTmemS = 256;           // S buffers at columns 256 and 384; 
 constexpr float kLazyRescale = 8.0f;
 constexpr int kMetaInts = 8;
 
+// How the page boxes of K or V lie in a slot: boxes of 2^rows_log2 rows x 2^chunks_log2 chunks of 64
+// columns; `step` bytes from 8 rows of K (16 of V) to the next, `chunk` from a chunk to the next.
+struct BoxLayout {
+  int rows_log2, chunks_log2, step, chunk;
+};
+
 struct Params {
   PagedBatch s;
   uint16_t* O;
@@ -65,7 +71,8 @@ struct Params {
   float* ws_O;   // [2 G][rows][256]: worker c's piece that began before its range (2 c) or in it (2 c + 1)
   float* ws_ml;  // [2 G][2][rows]: reference maximum (log2 units), sum
   int* ws_meta;  // [G][kMetaInts]
-  int Hq, Hkv, g_log2, box_log2;
+  int Hq, Hkv, g_log2;
+  BoxLayout k_box, v_box;
   float scale_log2;
   bool wide_stores;  // O is 32-byte aligned
 };
@@ -80,8 +87,7 @@ struct Shape {
   static constexpr int kRows = kPair ? 2 * kCtaRows : kCtaRows;
   static constexpr int kRowsLog2 = kPair ? 8 : 7;
   static constexpr int kParts = kPair ? 1 : 2;                           // slots of a tile
-  static constexpr int kKChunk = kPair ? 8 * 1024 : 16 * 1024;           // bytes of a slot's 64 columns
-  static constexpr int kVChunk = kPair ? 16 * 1024 : 8 * 1024;
+  static constexpr int kKChunksLog2 = kPair ? 2 : 1, kVChunksLog2 = kPair ? 1 : 2;  // chunks of a slot
   static constexpr int kReady = (kPair ? 2 : 1) * kSoftmaxWarps;
 };
 
@@ -333,10 +339,10 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 // A page box into this CTA's shared memory, completing on the leader's copy of `bar`.
 template <bool kPair>
-__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int col, int head, int row,
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int row, int chunk, int head,
                                          int page) {
-  if constexpr (kPair) tma_load_4d_pair(dst, map, cluster_addr(bar, 0), col, head, row, page);
-  else tma_load_4d(dst, map, bar, col, head, row, page);
+  if constexpr (kPair) tma_load_5d_pair(dst, map, cluster_addr(bar, 0), 0, row, chunk, head, page);
+  else tma_load_5d(dst, map, bar, 0, row, chunk, head, page);
 }
 
 template <bool kPair>
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  const int box_rows = 1 << p.box_log2;
+  const int box_rows = 1 << p.v_box.rows_log2;
   // whether key tile j holds rows behind the sequence's end that a page box brings in
   auto is_tail = [&](int len, int j) { return (len & (box_rows - 1)) != 0 && len / kKeyTile == j; };
   // the half of such a tile (64 rows) that holds them: a box lies in one half
@@ -401,20 +407,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (all lanes)
-    // A slot is 256 / box rows page boxes, one per lane: `wide` slots (128 rows x 2 chunks) and
-    // `narrow` ones (64 rows x 4 chunks); a pair's K and a single CTA's V are narrow.
-    const int n_tma = 256 >> p.box_log2;
-    const int nrow = (lane >> 2) << p.box_log2, nchunk = lane & 3, wrow = (lane >> 1) << p.box_log2, wchunk = lane & 1;
-    const int k_row = kPair ? nrow + 64 * (int)rank : wrow;  // this lane's row of a K tile
-    const int v_row = kPair ? wrow : nrow;                   // and of a V tile (single: + 64 per part)
+    // A slot's page boxes, one per lane, each of `rows` rows and some of the slot's chunks.
+    struct Box {
+      int row, chunk, to;  // this lane's first row and chunk, and where in the slot they go
+      bool on;
+    };
+    auto box_of = [&](int rows_log2, int chunks_log2, int slot_chunks_log2, int step_log2, int step, int chunk_bytes) {
+      const int across = slot_chunks_log2 - chunks_log2;  // log2 of the boxes side by side
+      Box x;
+      x.row = (lane >> across) << rows_log2;
+      x.chunk = (lane & ((1 << across) - 1)) << chunks_log2;
+      x.to = (x.row >> step_log2) * step + x.chunk * chunk_bytes;
+      x.on = x.row < (256 >> slot_chunks_log2);
+      return x;
+    };
+    const Box kb = box_of(p.k_box.rows_log2, p.k_box.chunks_log2, Sh::kKChunksLog2, 3, p.k_box.step, p.k_box.chunk);
+    const Box vb = box_of(p.v_box.rows_log2, p.v_box.chunks_log2, Sh::kVChunksLog2, 4, p.v_box.step, p.v_box.chunk);
+    const int k_row = kb.row + (kPair ? 64 * (int)rank : 0);  // this lane's row of a K tile
+    const int v_row = vb.row;                                 // and of a V tile (single: + 64 per part)
     const int page_mask = (1 << p.s.page_log2) - 1;
     uint32_t u = 0;  // slots issued: slot u % kSlots
     uint32_t it = 0, tails = 0;
     bool ok = true;
     for (Pieces w(p, start); !w.done() && ok; w.next(), ++it) {
       const int J = w.tiles();
-      auto page_of = [&](int row) -> int {  // a page that is not there: zeros (outside the tensor map)
-        if (lane >= n_tma || row >= w.q.len) return p.s.n_pages;
+      auto page_of = [&](int row, bool on) -> int {  // a page that is not there: zeros (outside the tensor map)
+        if (!on || row >= w.q.len) return p.s.n_pages;
         const int pg = paged_page(p.s, w.b, row);
         return pg < 0 ? p.s.n_pages : pg;
       };
@@ -436,15 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       // the pages of the next K tile, and of a K tile's V (used a step later), are looked up ahead
-      int pk = page_of(w.j0 * kKeyTile + k_row), pv[Sh::kParts] = {};
+      int pk = page_of(w.j0 * kKeyTile + k_row, kb.on), pv[Sh::kParts] = {};
       for (int step = 0; step <= J && ok; ++step) {
         const int j = w.j0 + step;
         int pk_next = 0, pv_next[Sh::kParts] = {};
-        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + k_row);
+        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + k_row, kb.on);
         if (step < J) {
 #pragma unroll
           for (int part = 0; part < Sh::kParts; ++part)
-            pv_next[part] = page_of(j * kKeyTile + v_row + 64 * part);
+            pv_next[part] = page_of(j * kKeyTile + v_row + 64 * part, vb.on);
 #pragma unroll
           for (int part = 0; part < Sh::kParts && ok; ++part) {
             ok = wait_slot();
@@ -452,15 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t s = u % kSlots;
             if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], (kPair ? 2 : 1) * kSlotBytes);
             __syncwarp();
-            if (lane < n_tma) {
-              uint8_t* dst = sRing + s * kSlotBytes;
-              if constexpr (kPair)
-                load_box<true>(dst + nchunk * Sh::kKChunk + nrow * 128, &map_k, &bar.full[s], nchunk * 64, w.h,
-                               (j * kKeyTile + k_row) & page_mask, pk);
-              else
-                load_box<false>(dst + wchunk * Sh::kKChunk + wrow * 128, &map_k, &bar.full[s],
-                                (2 * part + wchunk) * 64, w.h, (j * kKeyTile + k_row) & page_mask, pk);
-            }
+            if (kb.on)
+              load_box<kPair>(sRing + s * kSlotBytes + kb.to, &map_k, &bar.full[s], (j * kKeyTile + k_row) & page_mask,
+                              kPair ? kb.chunk : 2 * part + kb.chunk, w.h, pk);
             ++u;
           }
         }
@@ -472,9 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const uint32_t s = u % kSlots;
             const int in = ((j - 1) * kKeyTile + v_row + 64 * part) & page_mask;
-            uint8_t* dst = sRing + s * kSlotBytes +
-                           (kPair ? wchunk * Sh::kVChunk + wrow * 128 : nchunk * Sh::kVChunk + nrow * 128);
-            const int col = kPair ? 128 * (int)rank + wchunk * 64 : nchunk * 64;
+            uint8_t* dst = sRing + s * kSlotBytes + vb.to;
+            const int chunk = kPair ? 2 * (int)rank + vb.chunk : vb.chunk;
             if (tail_tile && (kPair || part == tail_part(w.q.len))) {
               uint64_t* tail = &bar.v_tail[tails++ & 1];
               if (lane == 0) {
@@ -482,11 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (rank == 0) mbar_arrive(&bar.full[s]);
               }
               __syncwarp();
-              if (lane < n_tma) tma_load_4d(dst, &map_v, tail, col, w.h, in, pv[part]);
+              if (vb.on) tma_load_5d(dst, &map_v, tail, 0, in, chunk, w.h, pv[part]);
             } else {
               if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bar.full[s], (kPair ? 2 : 1) * kSlotBytes);
               __syncwarp();
-              if (lane < n_tma) load_box<kPair>(dst, &map_v, &bar.full[s], col, w.h, in, pv[part]);
+              if (vb.on) load_box<kPair>(dst, &map_v, &bar.full[s], in, chunk, w.h, pv[part]);
             }
             ++u;
           }
@@ -521,14 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               ok = wait(&bar.full[s], (u / kSlots) & 1);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, 1024);
+              const uint64_t dk = smem_desc_sw128(sRa + s * kSlotBytes, 16, p.k_box.step);
               if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < 4 / Sh::kParts; ++c)
 #pragma unroll
                   for (int kk = 0; kk < 4; ++kk) {  // start addresses in 16-byte units
                     const uint64_t a = dq + (uint64_t)(((part * 2 + c) * kQChunk + kk * 32) >> 4);
-                    const uint64_t b = dk + (uint64_t)((c * Sh::kKChunk + kk * 32) >> 4);
+                    const uint64_t b = dk + (uint64_t)((c * p.k_box.chunk + kk * 32) >> 4);
                     if constexpr (kPair) mma_ss_pair(tS, a, b, idesc_s, (part | c | kk) != 0);
                     else mma_ss(tS, a, b, idesc_s, (part | c | kk) != 0);
                   }
@@ -556,12 +567,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : wait(&bar.p_ready[gj & 1], (gj >> 1) & 1);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, Sh::kVChunk, 1024);
+              const uint64_t dv = smem_desc_sw128(sRa + s * kSlotBytes, p.v_box.chunk, 1024);
               if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kKeyTile / 16 / Sh::kParts; ++kk) {
                   const uint32_t a = tP + (part * 4 + kk) * 8;
-                  const uint64_t b = dv + (uint64_t)((kk * 2048) >> 4);
+                  const uint64_t b = dv + (uint64_t)((kk * p.v_box.step) >> 4);
                   const uint32_t acc = (step > 1 || part > 0 || kk > 0) ? 1u : 0u;
                   if constexpr (kPair) mma_ts_pair(tmem, a, b, idesc_o, acc);
                   else mma_ts(tmem, a, b, idesc_o, acc);
@@ -678,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* slot = sRing + ((u + (2 * J - 1) * Sh::kParts + part) % kSlots) * kSlotBytes;
           for (int e = tid; e < (r1 - r0) * kRowPieces; e += 32 * kSoftmaxWarps) {
             const int r = r0 + e / kRowPieces - 64 * part, x = e % kRowPieces;
-            *reinterpret_cast<uint4*>(slot + (x >> 3) * Sh::kVChunk + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(slot + (x >> 3) * p.v_box.chunk + (r >> 4) * p.v_box.step + (r & 15) * 128 +
+                                      (x & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -987,6 +999,20 @@ size_t workspace_bytes_of(int sms) {
 // 3.6 ms.
 bool use_pairs(int B, int T, int g) { return (long long)T * g > (long long)kCtaRows * B; }
 
+// A box holds 64 rows of one chunk of 64 columns, or a page's.  A TMA copy costs some 95 cycles however
+// small, so that 2 KB boxes of 16-row pages would take longer than a pair's MMAs: there a box is 8 rows of
+// all of a pair's K chunks, which keeps the groups of 8 rows evenly apart, as the MMA's descriptor wants
+// them, or a page's V rows of all chunks, which are the keys of one MMA step.
+// (512 tokens over 8192 rows of 16-row pages 194 us against 236, one token of 16 sequences over 16384
+// rows each 68 against 72; larger pages gain nothing from it.)
+template <bool kPair>
+void box_layouts(int page, BoxLayout* k, BoxLayout* v) {
+  const bool small = page < 32;
+  const int rows = page < 64 ? log2_of(page) : 6, kc = Shape<kPair>::kKChunksLog2, vc = Shape<kPair>::kVChunksLog2;
+  *k = small && kPair ? BoxLayout{3, kc, 1024 << kc, 1024} : BoxLayout{rows, 0, 1024, kSlotBytes >> kc};
+  *v = small ? BoxLayout{4, vc, 2048 << vc, 2048} : BoxLayout{rows, 0, 2048, kSlotBytes >> vc};
+}
+
 template <bool kPair>
 hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, int sms,
                      cudaStream_t stream) {
@@ -1048,7 +1074,9 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.g_log2 = log2_of(Hq / Hkv);
-  p.box_log2 = page < 64 ? log2_of(page) : 6;
+  const bool pairs = use_pairs(B, T, Hq / Hkv);
+  if (pairs) box_layouts<true>(page, &p.k_box, &p.v_box);
+  else box_layouts<false>(page, &p.k_box, &p.v_box);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wide_stores = (reinterpret_cast<uintptr_t>(O) & 31u) == 0;
   CUtensorMap mq, mk, mv;
@@ -1060,13 +1088,14 @@ extern "C" hcadsa_status mla_paged_attn_fwd(const hcadsa_bf16* Q, long long q_ro
     if (!encode_tmap_bf16(&mq, 3, const_cast<hcadsa_bf16*>(Q), dims, strides, box, true)) return HCADSA_ERR_CUDA;
   }
   for (int v = 0; v < 2; ++v) {
-    const uint64_t dims[4] = {(uint64_t)kMlaD, (uint64_t)Hkv, (uint64_t)page, (uint64_t)n_pages};
-    const uint64_t strides[3] = {(uint64_t)kMlaD * 2, (uint64_t)Hkv * kMlaD * 2,
+    const BoxLayout& x = v ? p.v_box : p.k_box;
+    const uint64_t dims[5] = {64, (uint64_t)page, kMlaD / 64, (uint64_t)Hkv, (uint64_t)n_pages};
+    const uint64_t strides[4] = {(uint64_t)Hkv * kMlaD * 2, 64 * 2, (uint64_t)kMlaD * 2,
                                  (uint64_t)(v ? v_page_stride : k_page_stride) * 2};
-    const uint32_t box[4] = {64, 1, 1u << p.box_log2, 1};
-    if (!encode_tmap_bf16(v ? &mv : &mk, 4, const_cast<hcadsa_bf16*>(v ? V_pool : K_pool), dims, strides, box, true))
+    const uint32_t box[5] = {64, 1u << x.rows_log2, 1u << x.chunks_log2, 1, 1};
+    if (!encode_tmap_bf16(v ? &mv : &mk, 5, const_cast<hcadsa_bf16*>(v ? V_pool : K_pool), dims, strides, box, true))
       return HCADSA_ERR_CUDA;
   }
-  return use_pairs(B, T, Hq / Hkv) ? launch<true>(mq, mk, mv, p, sms, as_stream(stream))
-                                   : launch<false>(mq, mk, mv, p, sms, as_stream(stream));
+  return pairs ? launch<true>(mq, mk, mv, p, sms, as_stream(stream))
+               : launch<false>(mq, mk, mv, p, sms, as_stream(stream));
 }

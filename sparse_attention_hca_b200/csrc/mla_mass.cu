@@ -278,7 +278,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (all lanes)
-    // boxes of 128 K rows, one per lane: 8 rows x 4 chunks, or 128 / box rows x 1 chunk
+    // boxes of 128 K rows, one per lane: 8 rows x 4 chunks, or 128 / box rows x 1 chunk.  (Pages of 16 rows
+    // would take boxes of 2 KB, and a TMA copy costs some 95 cycles however small: 181 + 10 tokens over
+    // 4K-12K rows of such pages 80 us against 99.  With pages of 64 rows the larger boxes win, 72 against 78.)
     const bool groups = p.box_log2 == 3;
     const int krow = groups ? 8 * lane : (lane >> 2) << p.box_log2, kchunk = groups ? 0 : lane & 3;
     const int kboxes = groups ? 16 : 512 >> p.box_log2, kdst = krow * (p.k_group >> 3) + kchunk * p.k_chunk;
