@@ -6,7 +6,7 @@
 // touched; the i-th row that stays beyond it moves to the i-th freed place below it, so a cut of
 // m rows moves at most m rows, whatever the budget.
 //
-// One cluster of 2 to 8 CTAs per (sequence, K/V head).  The first CTAs share the rows below the
+// One cluster of 2 to 16 CTAs per (sequence, K/V head).  The first CTAs share the rows below the
 // budget, the others those beyond it, in contiguous slices, so every CTA counts either freed places
 // or rows that move.
 //   * Weights become 32-bit keys whose order is that of the weights (protected rows on top) and stay
@@ -22,7 +22,7 @@
 // What bounds it is latency: two dependent loads per row, three passes over the keys, four cluster
 // barriers.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
 // do not fit in shared memory are read from global memory again in every pass.
-// Measured (B200): 32 lists of 4224 rows cut to 4096 in 12.4 us, 4 lists of 131072 cut to 32768 in 27.
+// Measured (B200): 32 lists of 4224 rows cut to 4096 in 12.4 us, 4 lists of 131072 cut to 32768 in 23.
 #include <mutex>
 
 #include "mla_host.h"
@@ -32,7 +32,7 @@ namespace hcadsa {
 namespace {
 
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kPortable = 8, kLargest = 16;  // CTAs of a cluster
 constexpr int kGroupBins = 32, kBinGroups = kBins / kGroupBins;
 constexpr int kMaxSmemRows = 44 * 1024;
 constexpr uint32_t kSafe = 0xffffffffu;  // the key of a protected row
@@ -78,7 +78,7 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x, int lane) {
   return x;
 }
 
-template <int kThreads>
+template <int kThreads, int kMaxCluster>
 __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ uint4 keys[];
@@ -330,32 +330,66 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
   cluster_sync();  // no CTA ends while another reads its histograms
 }
 
-// SMs of the current device, the kernels' shared memory set up.
-int sms_of_device() {
+// The current device: its SMs, and how many clusters of 16 CTAs run on it at once.
+struct Device {
+  int sms, large;
+};
+
+template <int kThreads, int kMaxCluster>
+bool set_up() {
+  return cudaFuncSetAttribute(select_kernel<kThreads, kMaxCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMaxSmemRows * 4) == cudaSuccess &&
+         (kMaxCluster <= kPortable ||
+          cudaFuncSetAttribute(select_kernel<kThreads, kMaxCluster>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                               1) == cudaSuccess);
+}
+
+// `attr` has to live as long as the configuration.
+cudaLaunchConfig_t config_of(unsigned blocks, int cluster, int threads, size_t smem, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = cluster;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// The kernels' attributes are set on the first call.
+Device this_device() {
   static std::mutex mu;
-  static int cache[64] = {};
+  static Device cache[64] = {};
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return {};
   std::lock_guard<std::mutex> lock(mu);
-  if (!cache[dev]) {
-    int sms = 0;
-    const cudaFuncAttribute most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (!cache[dev].sms) {
+    int sms = 0, large = 0;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config_of(kLargest, kLargest, 1024, kMaxSmemRows * 4, &attr);
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(select_kernel<512>, most, kMaxSmemRows * 4) != cudaSuccess ||
-        cudaFuncSetAttribute(select_kernel<1024>, most, kMaxSmemRows * 4) != cudaSuccess) {
+        !set_up<512, kPortable>() || !set_up<1024, kPortable>() || !set_up<512, kLargest>() ||
+        !set_up<1024, kLargest>() ||
+        cudaOccupancyMaxActiveClusters(&large, select_kernel<1024, kLargest>, &cfg) != cudaSuccess) {
       launch_status();
-      return 0;
+      return {};
     }
-    cache[dev] = sms;
+    cache[dev] = {sms, large};
   }
   return cache[dev];
 }
 
 // A list of 4096 rows takes 12.4 us on four CTAs and 18.5 on two (32 lists at once); CTAs beyond one
-// per SM would wait for the first (35 us on eight).
-int cluster_of(long long lists, long long cap, int sms) {
+// per SM would wait for the first (35 us on eight).  Long lists go to 16 CTAs, as many as find room
+// for all of them at once: 131072 rows 23.4 us against 26.7 on eight, 65536 rows 18.8 against 20.5 (7
+// lists; 8 lists, for which there is no room, 35.4), but 32768 rows 17.9 against 16.4.
+int cluster_of(long long lists, long long cap, const Device& dev) {
+  if (cap >= 65536 && lists <= dev.large) return kLargest;
   int cluster = 2;
-  while (cluster < kMaxCluster && cap > 1024LL * cluster && 2 * cluster * lists <= sms) cluster *= 2;
+  while (cluster < kPortable && cap > 1024LL * cluster && 2 * cluster * lists <= dev.sms) cluster *= 2;
   return cluster;
 }
 
@@ -377,9 +411,9 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
       (reinterpret_cast<uintptr_t>(moves) & 7u) || !aligned4(new_len))
     return HCADSA_ERR_ALIGN;
   if (B == 0) return HCADSA_OK;
-  const int sms = sms_of_device();
-  if (sms <= 0) return HCADSA_ERR_CUDA;
-  const int cluster = cluster_of((long long)B * Hkv, cap, sms);
+  const Device dev = this_device();
+  if (dev.sms <= 0) return HCADSA_ERR_CUDA;
+  const int cluster = cluster_of((long long)B * Hkv, cap, dev);
   const long long blocks = (long long)B * Hkv * cluster;
   if (blocks > 2147483647LL) return HCADSA_ERR_UNSUPPORTED;
   // a side's share of the CTAs is rounded, so a slice may be half as long again as the average
@@ -399,20 +433,15 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   p.smem_rows = (int)(slice < kMaxSmemRows ? slice : kMaxSmemRows);
   p.vec = Hkv == 1 && aligned16(mass) && aligned16(pos);
   const size_t smem = (size_t)p.smem_rows * 4;
-  // 4096 rows per CTA and list: 512 threads 12.4 us, 1024 threads 14.4; 16384 rows: 28.7 and 26.8
+  // rows per CTA and list: 4096, 512 threads 12.4 us, 1024 threads 14.4; 8192, 23.4 and 24.6; 16384,
+  // 28.7 and 26.8
   const bool wide = cap > 8192LL * cluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-  cfg.blockDim = dim3(wide ? 1024 : 512, 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = config_of((unsigned)blocks, cluster, wide ? 1024 : 512, smem, &attr);
   cfg.stream = as_stream(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, wide ? select_kernel<1024> : select_kernel<512>, p) != cudaSuccess) return launch_status();
+  void (*kernel)(Params);
+  if (cluster > kPortable) kernel = wide ? select_kernel<1024, kLargest> : select_kernel<512, kLargest>;
+  else kernel = wide ? select_kernel<1024, kPortable> : select_kernel<512, kPortable>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return launch_status();
   return launch_status();
 }

@@ -295,6 +295,7 @@ SELECT = {
     "all_protected": dict(kv=[900], budget=300, sink=100, recent=200, page=64),
     "cluster": dict(kv=[40000, 33000], budget=9000, sink=8, recent=1000, page=128, Hkv=2),
     "cluster_ties": dict(kv=[50001], budget=25000, sink=8, recent=1000, page=16, levels=2),
+    "large_cluster": dict(kv=[70001, 66000], budget=30000, sink=8, recent=1000, page=64, levels=100),
     "special_values": dict(kv=[2000], budget=700, sink=4, recent=10, page=64, special=True),
     "wide_table": dict(kv=[300, 100], budget=100, sink=1, recent=2, page=16, width=4000),
     "nothing_to_do": dict(kv=[30, 64], budget=64, sink=1, recent=2, page=64, width=2),
@@ -355,18 +356,20 @@ def test_select_and_move(hd, name):
     assert torch.equal(again, moves)
 
 
-def test_select_rows_read_again(hd):
-    """A cache longer than the cluster's shared memory (8 x 48K rows) is read from memory in every pass."""
-    n, page, budget = 420001, 1024, 100000
+@pytest.mark.parametrize("n, lists", [(420001, 1), (900001, 1), (420001, 8)])
+def test_select_rows_read_again(hd, n, lists):
+    """Caches longer than their clusters' shared memory (44K rows per CTA, 16 CTAs for few lists, 8 for
+    more) are read from memory in every pass.  The lists are the same sequence, several times."""
+    page, budget = 1024, 100000
     width = -(-n // page)
     g = torch.Generator(device="cuda").manual_seed(1)
-    table = torch.randperm(width, generator=g, device="cuda").to(i32)[None]
+    table = torch.randperm(width, generator=g, device="cuda").to(i32)[None].repeat(lists, 1)
     mass = torch.randint(0, 1000, (width, page, 1), generator=g, device="cuda").float()
     pos = torch.zeros((width, page, 1), dtype=i32, device="cuda")
     i = torch.arange(n, device="cuda")
     at = table[0].long()[i // page], i % page
     pos[at] = i.to(i32)[:, None]
-    kv = torch.tensor([n], dtype=i32, device="cuda")
+    kv = torch.tensor([n] * lists, dtype=i32, device="cuda")
     moves, _ = hd.mla_evict_select(mass, pos, table, kv, None, budget, n_sink=16, n_recent=5000)
     hd.hcadsa_check_device_error()
     m = mass[at][:, 0].clone()
@@ -375,9 +378,10 @@ def test_select_rows_read_again(hd):
     keep = torch.zeros(n, dtype=torch.bool, device="cuda")
     keep[m.argsort(descending=True, stable=True)[:budget]] = True
     late, free = keep[budget:].nonzero()[:, 0] + budget, (~keep[:budget]).nonzero()[:, 0]
-    assert torch.equal(moves[0, 0, : len(late), 0].long(), late)
-    assert torch.equal(moves[0, 0, : len(free), 1].long(), free)
-    assert (moves[0, 0, len(late) :] == -1).all()
+    for b in range(lists):
+        assert torch.equal(moves[b, 0, : len(late), 0].long(), late)
+        assert torch.equal(moves[b, 0, : len(free), 1].long(), free)
+        assert (moves[b, 0, len(late) :] == -1).all()
 
 
 def test_device_errors_are_recorded_and_stay_inside(hd):
