@@ -350,8 +350,8 @@ hcadsa_status attn_gate_vha_fwd(const hcadsa_bf16* O, const hcadsa_bf16* cq, con
  *   pos, mass : [n_pages, page, Hkv] int32 / fp32, position and accumulated attention weight of every
  *              pool row
  * page is a power of two, 16 to 1024; d == 256; Hq / Hkv a power of two up to 128; the attention calls
- * take up to 2^23 new tokens (HCADSA_ERR_UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and mass need 4-byte alignment (moves: 8),
- * the bf16 tensors 16.  The lengths and tables are device data: a value out of range (a page that
+ * take up to 2^23 new tokens (HCADSA_ERR_UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and
+ * mass need 4-byte alignment (moves: 8), the bf16 tensors 16.  The lengths and tables are device data: a value out of range (a page that
  * is not in the pool, a length beyond max_pages * page, cu_q out of order) is recorded as
  * HCADSA_ERR_DEVICE_BOUNDS, and the rows it concerns are skipped or read as zeros; nothing outside
  * the tensors is touched.

@@ -27,11 +27,12 @@
 // leaves unnormalised fp32 rows and (max, sum) in the workspace -- at most two such pieces per
 // worker -- and combine_kernel merges them in list order: the result does not depend on timing.
 //
-// Measured (B200, 64 heads on one K/V head): 2048 tokens over 32768 rows 2.66 ms in a short run
-// (1.60 PFLOP/s), 3.01 ms when repeated (1.42 PFLOP/s; the power limit holds the clock at 1.43 GHz).
-// A product takes 2490 cycles of 2048 for its MMAs: the S MMAs read A and B from shared memory at
-// 128 bytes per cycle, its limit, next to the incoming tiles.  32 sequences of 1K-32K rows, one token
-// each: 105 us on the device, 5.4 TB/s.
+// Measured (B200, 64 heads on one K/V head): 2048 tokens over 32768 rows 2.8 ms in a short run
+// (1.52 PFLOP/s), 2.95 ms when repeated (1.44 PFLOP/s; the power limit holds the clock at 1.45 GHz).
+// A product takes about 2320 cycles of 2048 for its MMAs (the tensor pipe is busy 88 % of the active
+// cycles): the S MMAs read A and B from shared memory at 128 bytes per cycle, its limit, next to the
+// incoming tiles.  32 sequences of 1K-32K rows, one token each: 106 us on the device, 5.4 TB/s (113
+// repeated).
 //
 // Rows behind the end of a sequence in its last page may hold anything.  Their scores are replaced
 // before the softmax, and since 0 * NaN is NaN, the V rows of such a tile are cleared in shared
@@ -804,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // over many workers) it is one row, whose pieces the 8 warps divide among themselves and add up
 // through shared memory, in warp order.  Lane l holds columns 8 l .. 8 l + 7; the lanes read the
 // pieces' (max, sum) side by side, so the loads of the rows do not wait on one another.
-// (One sequence of 32768 rows, 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
+// (One sequence of 32768 rows cut into 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
 constexpr int kCombineWarps = 8;
 constexpr int kFewPieces = 8;
 constexpr int kMaxWorkers = 160;
@@ -994,8 +995,8 @@ size_t workspace_bytes_of(int sms) {
 // Pairs take row tiles of 256 rows and load half the K and V per product; single CTAs take row tiles
 // of 128 rows, so a sequence that has no more rows than that (a decode step) costs half the MMA time.
 // Both give right results for every batch; the host only knows the averages.  Measured, pairs and
-// single CTAs: 32 decode steps over 1K-32K rows 117 and 105 us; two 389-token chunks next to 22
-// decode steps (266 rows per sequence on average) 210 and 233 us; 2048 tokens over 32768 rows 3.0 and
+// single CTAs: 32 decode steps over 1K-32K rows 116 and 106 us; two 389-token chunks next to 22
+// decode steps (266 rows per sequence on average) 211 and 233 us; 2048 tokens over 32768 rows 2.8 and
 // 3.6 ms.
 bool use_pairs(int B, int T, int g) { return (long long)T * g > (long long)kCtaRows * B; }
 

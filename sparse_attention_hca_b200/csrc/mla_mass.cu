@@ -21,8 +21,8 @@
 // the pairs.  A block that several pairs share leaves partial sums in the workspace, which
 // add_kernel adds up in list order; every row's mass gets exactly one addition per call.
 //
-// Measured (B200, 64 heads on one K/V head): 1021 tokens over 16381 rows 397 us in a short run (1.34
-// PFLOP/s), 465 us when repeated (power limit); the MMAs and loads alone, without the sums, take 313.
+// Measured (B200, 64 heads on one K/V head): 1021 tokens over 16381 rows 380 us in a short run (1.40
+// PFLOP/s), 446 us when repeated (power limit); the MMAs and loads alone, without the sums, take 313.
 // Products of 256 columns (two S buffers) took 412 us, K held in TMEM as the A operand 417.  A decode
 // step of 32 sequences of 1K-32K rows: 55 us for the kernel (5.2 TB/s), 61 with zeroing and adding up.
 #include <mutex>
