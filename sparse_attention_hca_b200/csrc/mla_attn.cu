@@ -281,7 +281,8 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   const int n = most < n_workers ? (int)most : n_workers;
   if (tid == 0) out->count = 0;
   if (worker >= n) return;
-  const long long x0 = all * worker / n, x1 = all * (worker + 1) / n, share = all / n;
+  const long long x0 = all * worker / n, x1 = all * (worker + 1) / n;
+  const long long share = all / n;  // (the same for all workers, so that neighbours agree on a cut)
   // f(sequence, its products [from, upto)) for every sequence, all threads side by side
   auto each = [&](auto&& f) {
     long long done = 0;
@@ -305,7 +306,8 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
       for (int e = 0; e < 2; ++e) {
         const long long x = e ? x1 : x0;
         if (from <= x && x < upto)
-          cut[e] = snap(seq_tiles(paged_seq(p.s, b, false), tq_log2), from, (upto - from) / p.Hkv, x, share);
+          cut[e] = snap(seq_tiles(paged_seq(p.s, b, false), tq_log2), from,
+                        (upto - from) / p.Hkv, x, share);
       }
     });
     __syncthreads();
@@ -801,13 +803,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of the maxima,
 //     O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
 // Every block lists the row tiles to merge from the workers' records and takes its share of the work
-// items: with up to kFewPieces pieces an item is 8 rows, one warp each; with more (a long cache cut
-// over many workers) it is one row, whose pieces the 8 warps divide among themselves and add up
-// through shared memory, in warp order.  Lane l holds columns 8 l .. 8 l + 7; the lanes read the
+// items: with up to `few` pieces an item is 8 rows, one warp each; with more (a long cache cut over
+// many workers) it is one row, whose pieces the 8 warps divide among themselves and add up through
+// shared memory, in warp order.  `few` is 8, or 32 where there are more rows than blocks, which one
+// warp per row keeps busy (124 tokens over 1747 rows, 16 K/V heads: 33.5 us
+// against 43).  Lane l holds columns 8 l .. 8 l + 7; the lanes read the
 // pieces' (max, sum) side by side, so the loads of the rows do not wait on one another.
 // (One sequence of 32768 rows cut into 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
 constexpr int kCombineWarps = 8;
-constexpr int kFewPieces = 8;
 constexpr int kMaxWorkers = 160;
 
 // Columns 8 l .. 8 l + 7 of piece k's row, added to acc with weight w.
@@ -824,7 +827,7 @@ __device__ __forceinline__ void add_piece(const float4& a, const float4& b, floa
   }
 }
 
-__global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Params p, int n_workers, int n_rows) {
+__global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Params p, int n_workers, int n_rows, int few_pieces) {
   __shared__ int pieces_of[kMaxWorkers], first_item[kMaxWorkers + 1];
   __shared__ int4 tile_of[kMaxWorkers];  // first packed token, tokens, K/V head
   __shared__ uint32_t ends[kMaxWorkers / 32];  // bit c: worker c's first piece, if any, is the last of its row tile
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Pa
       const int n = min(c, n_workers - 1) - tid + 1;
       pieces_of[tid] = n;
       tile_of[tid] = make_int4(mine[2], mine[3], mine[4], 0);
-      items = n <= kFewPieces ? (rows + kCombineWarps - 1) / kCombineWarps : rows;
+      items = n <= few_pieces ? (rows + kCombineWarps - 1) / kCombineWarps : rows;
     }
     first_item[tid + 1] = items;
     if (tid == 0) first_item[0] = 0;
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Pa
     }
     const int4 tile = tile_of[c];
     const int n = pieces_of[c];
-    const bool few = n <= kFewPieces;
+    const bool few = n <= few_pieces;
     const int row = few ? (item - first_item[c]) * kCombineWarps + warp : item - first_item[c];
     const int tok = row >> p.g_log2;
     auto slot = [&](int k) { return (size_t)(k ? 2 * (c + k) : 2 * c + 1); };
@@ -902,8 +905,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Pa
       }
       M = l > 0.0f ? m : -INFINITY;
 #pragma unroll
-      for (int o = kFewPieces / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      M = __shfl_sync(0xffffffffu, M, 0);  // (the first kFewPieces lanes hold the pieces)
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       const float w_mine = l > 0.0f ? exp2f(m - M) : 0.0f;
       den = 0.0f;
 #pragma unroll 4
@@ -1031,7 +1033,9 @@ hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
-  return launch_after(combine_kernel, dim3(4 * sms), 32 * kCombineWarps, stream, p, workers, (int)Shape<kPair>::kRows);
+  const int blocks = 4 * sms, few = (long long)p.s.T * p.Hq > blocks ? 32 : 8;
+  return launch_after(combine_kernel, dim3(blocks), 32 * kCombineWarps, stream, p, workers, (int)Shape<kPair>::kRows,
+                      few);
 }
 
 }  // namespace
