@@ -159,6 +159,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2) {
 struct Start {
   long long count;  // products of this worker
   int b, h, i, j;   // where they begin
+  PagedSeq q;       // sequence b
 };
 
 // Walks a worker's pieces: runs of key tiles of one row tile.
@@ -177,7 +178,8 @@ struct Walk {
     i = s.i;
     j0 = s.j;
     if (left > 0) {
-      load();
+      q = s.q;
+      t = seq_tiles(q, tq_log2);
       cut();
     }
   }
@@ -316,7 +318,8 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   if (tid == 0) out->count = hi - lo;
   each([&](int b, long long from, long long upto) {
     if (from <= lo && lo < upto) {
-      const SeqTiles t = seq_tiles(paged_seq(p.s, b, false), tq_log2);
+      out->q = paged_seq(p.s, b, false);
+      const SeqTiles t = seq_tiles(out->q, tq_log2);
       const long long per_head = (upto - from) / p.Hkv, r = lo - from;
       out->b = b;
       out->h = (int)(r / per_head);
@@ -396,10 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
+  __syncwarp();
+  if constexpr (kPair) cluster_arrive();
   find_start<kPair>(p, Sh::kRowsLog2 - p.g_log2, worker, n_workers, &start);
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
+  if constexpr (kPair) cluster_wait();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const int box_rows = 1 << p.v_box.rows_log2;
@@ -456,16 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      // the pages of the next K tile, and of a K tile's V (used a step later), are looked up ahead
+      // the pages of the next K tile, and of a K tile's V (used a step later), are looked up once this
+      // step's loads are on their way
       int pk = page_of(w.j0 * kKeyTile + k_row, kb.on), pv[Sh::kParts] = {};
       for (int step = 0; step <= J && ok; ++step) {
         const int j = w.j0 + step;
-        int pk_next = 0, pv_next[Sh::kParts] = {};
-        if (step + 1 < J) pk_next = page_of((j + 1) * kKeyTile + k_row, kb.on);
         if (step < J) {
-#pragma unroll
-          for (int part = 0; part < Sh::kParts; ++part)
-            pv_next[part] = page_of(j * kKeyTile + v_row + 64 * part, vb.on);
 #pragma unroll
           for (int part = 0; part < Sh::kParts && ok; ++part) {
             ok = wait_slot();
@@ -505,9 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++u;
           }
         }
-        pk = pk_next;
+        if (step + 1 < J) pk = page_of((j + 1) * kKeyTile + k_row, kb.on);
+        if (step < J) {
 #pragma unroll
-        for (int part = 0; part < Sh::kParts; ++part) pv[part] = pv_next[part];
+          for (int part = 0; part < Sh::kParts; ++part) pv[part] = page_of(j * kKeyTile + v_row + 64 * part, vb.on);
+        }
       }
     }
   } else if (warp == 1) {

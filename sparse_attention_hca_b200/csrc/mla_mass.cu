@@ -97,6 +97,7 @@ struct SeqBlocks {
 struct Start {
   long long count;
   int b, h, k, t;
+  PagedSeq q;  // sequence b
 };
 
 // Walks a pair's pieces: runs of Q tiles against one block.
@@ -112,7 +113,7 @@ struct Walk {
     h = st.h;
     k = st.k;
     if (left > 0) {
-      load();
+      load(st.q);
       cut(st.t);
     }
   }
@@ -134,7 +135,7 @@ struct Walk {
             left = 0;
             return;
           }
-          load();
+          load(paged_seq(p.s, b, false));
         } while (s.blocks() == 0);
       }
     }
@@ -142,8 +143,8 @@ struct Walk {
   }
 
  private:
-  __device__ void load() {
-    q = paged_seq(p.s, b, false);
+  __device__ void load(const PagedSeq& seq) {
+    q = seq;
     s.base = q.base;
     s.n = q.n;
     s.len = q.len;
@@ -162,8 +163,7 @@ struct Walk {
 __device__ __forceinline__ void find_start(const Params& p, int worker, int n_workers, Start* out) {
   __shared__ long long sums[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto seq = [&](int b, bool report) -> SeqBlocks {
-    const PagedSeq q = paged_seq(p.s, b, report);
+  auto blocks_of = [&](const PagedSeq& q) -> SeqBlocks {
     SeqBlocks s;
     s.base = q.base;
     s.n = q.n;
@@ -173,7 +173,7 @@ __device__ __forceinline__ void find_start(const Params& p, int worker, int n_wo
   };
   auto work_of = [&](int b, bool report) -> long long {
     if (b >= p.s.B) return 0;
-    const SeqBlocks s = seq(b, report);
+    const SeqBlocks s = blocks_of(paged_seq(p.s, b, report));
     return s.before(s.blocks()) * p.Hkv;
   };
   auto scan = [&](long long x, long long& total) -> long long {  // inclusive prefix over the threads
@@ -195,28 +195,33 @@ __device__ __forceinline__ void find_start(const Params& p, int worker, int n_wo
   };
   long long mine = 0, all;
   for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
-  scan(mine, all);
+  const long long mine_to = scan(mine, all);
   const int n = all < n_workers ? (int)all : n_workers;
   const long long lo = worker < n ? all * worker / n : 0, hi = worker < n ? all * (worker + 1) / n : 0;
   if (tid == 0) out->count = hi - lo;
-  long long done = 0;
-  for (int b0 = 0; b0 < p.s.B && hi > lo; b0 += kThreads) {
-    const long long w = p.s.B <= kThreads ? mine : work_of(b0 + tid, false);
-    long long total;
-    const long long upto = done + scan(w, total), from = upto - w;
-    if (from <= lo && lo < upto) {
-      const SeqBlocks s = seq(b0 + tid, false);
-      const long long per_head = w / p.Hkv, r = lo - from;
-      out->b = b0 + tid;
-      out->h = (int)(r / per_head);
-      const long long in = r - out->h * per_head;
-      out->k = s.find(in);
-      out->t = s.first_tile(out->k) + (int)(in - s.before(out->k));
-    }
-    done += total;
-    if (done > lo) break;
+  if (hi <= lo) return;
+  auto find = [&](int b, long long from, long long upto) {  // sequence b's products are [from, upto)
+    if (lo < from || lo >= upto) return;
+    out->q = paged_seq(p.s, b, false);
+    const SeqBlocks s = blocks_of(out->q);
+    const long long per_head = (upto - from) / p.Hkv, r = lo - from;
+    out->b = b;
+    out->h = (int)(r / per_head);
+    const long long in = r - out->h * per_head;
+    out->k = s.find(in);
+    out->t = s.first_tile(out->k) + (int)(in - s.before(out->k));
+  };
+  if (p.s.B <= kThreads) {  // known from the first pass
+    find(tid, mine_to - mine, mine_to);
+    return;
   }
-  __syncthreads();
+  long long done = 0;
+  for (int b0 = 0; b0 < p.s.B && done <= lo; b0 += kThreads) {
+    long long total;
+    const long long w = work_of(b0 + tid, false), upto = done + scan(w, total);
+    find(b0 + tid, upto - w, upto);
+    done += total;
+  }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -268,10 +273,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_k);
   }
   if (warp == 1) tmem_alloc_pair(&tmem_base_sh, 512);
+  __syncwarp();
+  cluster_arrive();
   find_start(p, worker, n_workers, &start);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
+  cluster_wait();  // barriers and TMEM of both CTAs exist before any cross-CTA operation
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const int page_mask = (1 << p.s.page_log2) - 1;
