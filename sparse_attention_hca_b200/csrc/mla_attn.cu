@@ -21,9 +21,10 @@
 // O).  P is rounded to bf16, the type the tensor cores take, after its sum was taken in fp32.
 //
 // Schedule: the (row tile, key tile) products of the whole batch form one list -- sequence, K/V
-// head, row tile, key tile -- whose length follows in closed form from the lengths.  Worker c of G
-// takes the products [c N / G, (c+1) N / G): equal work for prompts, chunks and single tokens alike,
-// decided on the device (the host never sees the lengths).  A row tile that several workers share
+// head, row tile, key tile -- whose length follows in closed form from the lengths (in long lists a
+// row tile also takes some places for its output, see kTileCost).  Worker c of G takes the places
+// [c N / G, (c+1) N / G): equal work for prompts, chunks and single tokens alike, decided on the device
+// (the host never sees the lengths).  A row tile that several workers share
 // leaves unnormalised fp32 rows and (max, sum) in the workspace -- at most two such pieces per
 // worker -- and combine_kernel merges them in list order: the result does not depend on timing.
 //
@@ -105,6 +106,7 @@ struct __align__(8) Barriers {
 // One sequence's part of the list (of one K/V head).
 struct SeqTiles {
   int base, n, len, tq_log2;
+  int extra;  // what a row tile weighs in the list besides its products
   __host__ __device__ int row_tiles() const { return (n + (1 << tq_log2) - 1) >> tq_log2; }
   // key tiles of row tile i: up to the last row its last token sees.  A sequence declared shorter
   // than its chunk (base < 0) has rows that see nothing; its row tiles take every key tile, at
@@ -135,20 +137,31 @@ struct SeqTiles {
     }
     return sum;
   }
-  // the row tile that holds product w of the list
+  // where row tile i begins in the list
+  __host__ __device__ long long start(int i) const { return before(i) + (long long)extra * i; }
+  // the row tile that holds place w of the list
   __host__ __device__ int find(long long w) const {
     int lo = 0, hi = row_tiles();
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (before(mid) <= w) lo = mid;
+      if (start(mid) <= w) lo = mid;
       else hi = mid;
     }
     return lo;
   }
 };
 
-__device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2) {
+// A pair's row tile costs its output (4-5 us) besides its products (1.3 us each), so in lists that give
+// every pair 8 products or more a tile weighs as much as this many more, which come first in it.  (3
+// sequences of 844 tokens over up to 1749 rows next to 26 single tokens, 16 heads: 57 us against 84; 361
+// tokens over 10164 rows, 16 heads, 61 against 62; 2 is 2-4 % slower there, 6 10 %.)  Not the tile of a
+// sequence with at most 32 rows to write (weighed as well, 2 chunks next to 22 single tokens of 8 rows took
+// 1 % longer; with single tokens of 64 rows not weighed, 29 sequences took 90 us against 82).
+constexpr int kTileCost = 3;
+
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2, bool weigh) {
   SeqTiles t;
+  t.extra = weigh && 8 * q.n > (1 << tq_log2) ? kTileCost : 0;
   t.base = q.base;
   t.n = q.n;
   t.len = q.len;
@@ -157,8 +170,9 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedSeq& q, int tq_log2) {
 }
 
 struct Start {
-  long long count;  // products of this worker
-  int b, h, i, j;   // where they begin
+  long long count;  // this worker's share of the list
+  int b, h, i, at;  // where it begins: `at` places into row tile i
+  bool weigh;       // whether row tiles weigh more than their products
   PagedSeq q;       // sequence b
 };
 
@@ -167,7 +181,8 @@ template <int kRowsLog2>
 struct Walk {
   const Params& p;
   long long left;
-  int b, h, i, j0, j1, n_keys, tq_log2;
+  int b, h, i, at, j0, j1, n_keys, tq_log2;
+  bool weigh;
   PagedSeq q;
   SeqTiles t;
   __device__ Walk(const Params& p_, const Start& s) : p(p_) {
@@ -176,10 +191,11 @@ struct Walk {
     b = s.b;
     h = s.h;
     i = s.i;
-    j0 = s.j;
+    at = s.at;
+    weigh = s.weigh;
     if (left > 0) {
       q = s.q;
-      t = seq_tiles(q, tq_log2);
+      t = seq_tiles(q, tq_log2, weigh);
       cut();
     }
   }
@@ -187,9 +203,9 @@ struct Walk {
   __device__ int tiles() const { return j1 - j0; }
   __device__ int first_token() const { return i << tq_log2; }
   __device__ void next() {
-    left -= j1 - j0;
+    left -= j1 + t.extra - at;
     if (left <= 0) return;
-    j0 = 0;
+    at = 0;
     if (++i == t.row_tiles()) {
       i = 0;
       if (++h == p.Hkv) {
@@ -209,12 +225,14 @@ struct Walk {
  private:
   __device__ void load() {
     q = paged_seq(p.s, b, false);
-    t = seq_tiles(q, tq_log2);
+    t = seq_tiles(q, tq_log2, weigh);
   }
-  __device__ void cut() {
+  __device__ void cut() {  // places [0, t.extra) of a row tile hold no product
     n_keys = t.key_tiles(i);
-    const long long e = (long long)j0 + left;
+    const long long e = at + left - t.extra;
+    j0 = at > t.extra ? at - t.extra : 0;
     j1 = e < n_keys ? (int)e : n_keys;
+    if (j1 <= j0) left = 0;  // the share ends before the tile's first product
   }
 };
 
@@ -233,8 +251,8 @@ __device__ __forceinline__ long long snap(const SeqTiles& t, long long from, lon
   const long long in = (x - from) % per_head;
   const int i = t.find(in), n = t.key_tiles(i);
   if (n > kShortTile || n > 2 * share) return x;
-  const long long j = in - t.before(i);
-  return x - j + (2 * j >= n ? n : 0);
+  const long long j = in - t.start(i);
+  return x - j + (2 * j >= n + t.extra ? n + t.extra : 0);
 }
 
 // Every thread of the CTA: this worker's share of the list.
@@ -243,10 +261,11 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   __shared__ long long sums[kThreads / 32];
   __shared__ long long cut[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool weigh = false;
   auto work_of = [&](int b, bool report) -> long long {
     if (b >= p.s.B) return 0;
-    const SeqTiles t = seq_tiles(paged_seq(p.s, b, report), tq_log2);
-    return t.n > 0 ? t.before(t.row_tiles()) * p.Hkv : 0;
+    const SeqTiles t = seq_tiles(paged_seq(p.s, b, report), tq_log2, weigh);
+    return t.n > 0 ? t.start(t.row_tiles()) * p.Hkv : 0;
   };
   // inclusive prefix over the CTA's threads, and its total
   auto scan = [&](long long x, long long& total) -> long long {
@@ -268,7 +287,13 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   };
   long long mine = 0, all;
   for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
-  const long long mine_to = scan(mine, all);
+  long long mine_to = scan(mine, all);
+  if (kPair && all >= 8LL * n_workers) {
+    weigh = true;
+    mine = 0;
+    for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, false);
+    mine_to = scan(mine, all);
+  }
   // A short list goes to as many workers as it has products, so that consecutive pieces of a row
   // tile always lie with consecutive workers; long row tiles to fewer.  Merging costs about 1/12 of
   // a product per piece, so a tile of k products is best cut into pieces of sqrt(k / 12).  (One token
@@ -308,7 +333,7 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
       for (int e = 0; e < 2; ++e) {
         const long long x = e ? x1 : x0;
         if (from <= x && x < upto)
-          cut[e] = snap(seq_tiles(paged_seq(p.s, b, false), tq_log2), from,
+          cut[e] = snap(seq_tiles(paged_seq(p.s, b, false), tq_log2, weigh), from,
                         (upto - from) / p.Hkv, x, share);
       }
     });
@@ -319,13 +344,14 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   each([&](int b, long long from, long long upto) {
     if (from <= lo && lo < upto) {
       out->q = paged_seq(p.s, b, false);
-      const SeqTiles t = seq_tiles(out->q, tq_log2);
+      const SeqTiles t = seq_tiles(out->q, tq_log2, weigh);
       const long long per_head = (upto - from) / p.Hkv, r = lo - from;
       out->b = b;
       out->h = (int)(r / per_head);
       const long long in = r - out->h * per_head;
       out->i = t.find(in);
-      out->j = (int)(in - t.before(out->i));
+      out->at = (int)(in - t.start(out->i));
+      out->weigh = weigh;
     }
   });
 }
