@@ -152,9 +152,10 @@ struct SeqTiles {
 };
 
 // A pair's row tile costs its output (4-5 us) besides its products (1.3 us each), so in lists that give
-// every pair 8 products or more a tile weighs as much as this many more, which come first in it.  (3
+// every pair 2 products or more a tile weighs as much as this many more, which come first in it.  (3
 // sequences of 844 tokens over up to 1749 rows next to 26 single tokens, 16 heads: 57 us against 84; 361
-// tokens over 10164 rows, 16 heads, 61 against 62; 2 is 2-4 % slower there, 6 10 %.)  Not the tile of a
+// tokens over 10164 rows, 16 heads, 61 against 62; 512 tokens from nothing, 64 heads, 33 against 37; a
+// weight of 2 is 2-4 % slower in the first two, 6 10 %.)  Not the tile of a
 // sequence with at most 32 rows to write (weighed as well, 2 chunks next to 22 single tokens of 8 rows took
 // 1 % longer; with single tokens of 64 rows not weighed, 29 sequences took 90 us against 82).
 constexpr int kTileCost = 3;
@@ -288,7 +289,7 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   long long mine = 0, all;
   for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, blockIdx.x == 0);
   long long mine_to = scan(mine, all);
-  if (kPair && all >= 8LL * n_workers) {
+  if (kPair && all >= 2LL * n_workers) {
     weigh = true;
     mine = 0;
     for (int b = tid; b < p.s.B; b += kThreads) mine += work_of(b, false);
