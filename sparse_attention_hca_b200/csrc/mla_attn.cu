@@ -836,9 +836,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // items: with up to `few` pieces an item is 8 rows, one warp each; with more (a long cache cut over
 // many workers) it is one row, whose pieces the 8 warps divide among themselves and add up through
 // shared memory, in warp order.  `few` is 8, or 32 where there are more rows than blocks, which one
-// warp per row keeps busy (124 tokens over 1747 rows, 16 K/V heads: 33.5 us
-// against 43).  Lane l holds columns 8 l .. 8 l + 7; the lanes read the
-// pieces' (max, sum) side by side, so the loads of the rows do not wait on one another.
+// warp per row keeps busy (124 tokens over 1747 rows, 16 K/V heads: 33.5 us against 43).  Lane l holds
+// columns 8 l .. 8 l + 7; the lanes read the pieces' (max, sum) side by side, so the loads of the rows
+// do not wait on one another.
 // (One sequence of 32768 rows cut into 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
 constexpr int kCombineWarps = 8;
 constexpr int kMaxWorkers = 160;
@@ -857,7 +857,8 @@ __device__ __forceinline__ void add_piece(const float4& a, const float4& b, floa
   }
 }
 
-__global__ void __launch_bounds__(32 * kCombineWarps, 4) combine_kernel(const Params p, int n_workers, int n_rows, int few_pieces) {
+__global__ void __launch_bounds__(32 * kCombineWarps, 4)
+    combine_kernel(const Params p, int n_workers, int n_rows, int few_pieces) {
   __shared__ int pieces_of[kMaxWorkers], first_item[kMaxWorkers + 1];
   __shared__ int4 tile_of[kMaxWorkers];  // first packed token, tokens, K/V head
   __shared__ uint32_t ends[kMaxWorkers / 32];  // bit c: worker c's first piece, if any, is the last of its row tile

@@ -79,7 +79,7 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x, int lane) {
 }
 
 template <int kThreads, int kMaxCluster>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) select_kernel(const Params p) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ uint4 keys[];
   __shared__ Shared<kWarps> sh;
@@ -371,8 +371,8 @@ Device this_device() {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config_of(kLargest, kLargest, 1024, kMaxSmemRows * 4, &attr);
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        !set_up<512, kPortable>() || !set_up<1024, kPortable>() || !set_up<512, kLargest>() ||
-        !set_up<1024, kLargest>() ||
+        !set_up<256, kPortable>() || !set_up<512, kPortable>() || !set_up<1024, kPortable>() ||
+        !set_up<512, kLargest>() || !set_up<1024, kLargest>() ||
         cudaOccupancyMaxActiveClusters(&large, select_kernel<1024, kLargest>, &cfg) != cudaSuccess) {
       launch_status();
       return {};
@@ -383,13 +383,16 @@ Device this_device() {
 }
 
 // A list of 4096 rows takes 12.4 us on four CTAs and 18.5 on two (32 lists at once); CTAs beyond one
-// per SM would wait for the first (35 us on eight).  Long lists go to 16 CTAs, as many as find room
+// per SM would wait for the first (35 us on eight), so beyond that a CTA gets 4096 rows (80 lists of 32768
+// rows of 8 K/V heads 77 us, 119 on two CTAs each).  Long lists go to 16 CTAs, as many as find room
 // for all of them at once: 131072 rows 23.4 us against 26.7 on eight, 65536 rows 18.8 against 20.5 (7
 // lists; 8 lists, for which there is no room, 35.4), but 32768 rows 17.9 against 16.4.
 int cluster_of(long long lists, long long cap, const Device& dev) {
   if (cap >= 65536 && lists <= dev.large) return kLargest;
   int cluster = 2;
-  while (cluster < kPortable && cap > 1024LL * cluster && 2 * cluster * lists <= dev.sms) cluster *= 2;
+  while (cluster < kPortable && cap > 1024LL * cluster &&
+         (2 * cluster * lists <= dev.sms || cap > 4096LL * cluster))
+    cluster *= 2;
   return cluster;
 }
 
@@ -416,8 +419,10 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   const int cluster = cluster_of((long long)B * Hkv, cap, dev);
   const long long blocks = (long long)B * Hkv * cluster;
   if (blocks > 2147483647LL) return HCADSA_ERR_UNSUPPORTED;
-  // a side's share of the CTAs is rounded, so a slice may be half as long again as the average
-  const long long slice = (cap * 3 / 2 / cluster + 64 + 3) / 4 * 4;
+  // a side's share of the CTAs is rounded, so a slice may be half as long again as the average, and of two
+  // CTAs one may get nearly all (80 lists of 32768 rows, cut to 4096 on two CTAs each and
+  // read again in every pass, took 334 us instead of 119)
+  const long long slice = ((cluster == 2 ? cap : cap * 3 / 2 / cluster) + 64 + 3) / 4 * 4;
   Params p;
   p.s = paged_batch(table, nullptr, kv_len, B, 0, n_pages, page, max_pages);
   p.mass = mass;
@@ -434,13 +439,15 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   p.vec = Hkv == 1 && aligned16(mass) && aligned16(pos);
   const size_t smem = (size_t)p.smem_rows * 4;
   // rows per CTA and list: 4096, 512 threads 12.4 us, 1024 threads 14.4; 8192, 23.4 and 24.6; 16384,
-  // 28.7 and 26.8
-  const bool wide = cap > 8192LL * cluster;
+  // 28.7 and 26.8.  More CTAs than SMs: blocks of 256 threads, four to an SM (256 lists of 2048 rows 19.5 us
+  // against 45 with 512 threads).
+  const bool wide = cap > 8192LL * cluster, many = blocks > dev.sms;
   cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = config_of((unsigned)blocks, cluster, wide ? 1024 : 512, smem, &attr);
+  cudaLaunchConfig_t cfg = config_of((unsigned)blocks, cluster, wide ? 1024 : many ? 256 : 512, smem, &attr);
   cfg.stream = as_stream(stream);
   void (*kernel)(Params);
   if (cluster > kPortable) kernel = wide ? select_kernel<1024, kLargest> : select_kernel<512, kLargest>;
+  else if (many && !wide) kernel = select_kernel<256, kPortable>;
   else kernel = wide ? select_kernel<1024, kPortable> : select_kernel<512, kPortable>;
   if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return launch_status();
   return launch_status();

@@ -296,6 +296,8 @@ SELECT = {
     "cluster": dict(kv=[40000, 33000], budget=9000, sink=8, recent=1000, page=128, Hkv=2),
     "cluster_ties": dict(kv=[50001], budget=25000, sink=8, recent=1000, page=16, levels=2),
     "large_cluster": dict(kv=[70001, 66000], budget=30000, sink=8, recent=1000, page=64, levels=100),
+    "many_lists": dict(kv=[300, 17, 2100] * 30, budget=100, sink=4, recent=20, page=16, Hkv=2, levels=50),
+    "many_longer_lists": dict(kv=[9000, 4000] * 40, budget=300, sink=4, recent=20, page=64, levels=200),
     "special_values": dict(kv=[2000], budget=700, sink=4, recent=10, page=64, special=True),
     "wide_table": dict(kv=[300, 100], budget=100, sink=1, recent=2, page=16, width=4000),
     "nothing_to_do": dict(kv=[30, 64], budget=64, sink=1, recent=2, page=64, width=2),
