@@ -74,6 +74,7 @@ struct Params {
   float* ws_ml;  // [2 G][2][rows]: reference maximum (log2 units), sum
   int* ws_meta;  // [G][kMetaInts]
   int Hq, Hkv, g_log2;
+  int piece_rows;  // rows of an average row tile where the batch has more rows than the merge has blocks, or 0
   BoxLayout k_box, v_box;
   float scale_log2;
   bool wide_stores;  // O is 32-byte aligned
@@ -296,14 +297,17 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
     mine_to = scan(mine, all);
   }
   // A short list goes to as many workers as it has products, so that consecutive pieces of a row
-  // tile always lie with consecutive workers; long row tiles to fewer.  Merging costs about 1/12 of
-  // a product per piece, so a tile of k products is best cut into pieces of sqrt(k / 12).  (One token
-  // over 16K, 32K, 128K rows: 20.5, 24.6, 41.2 us against 23.3, 30.0, 45.1 on all workers; a constant
-  // of 8 or 16 is up to 2 us slower.)
+  // tile always lie with consecutive workers; where merging costs more, to fewer.  A piece costs the
+  // merge about 1/12 of a product, so a tile of k products is best cut into pieces of sqrt(k / 12).  (One
+  // token over 16K, 32K, 128K rows: 20.5, 24.6, 41.2 us against 23.3, 30.0, 45.1 on all workers; a constant
+  // of 8 or 16 is up to 2 us slower.)  Where many rows are merged it also costs their bytes, 1/6000 of a
+  // product per row of every piece (124 tokens over 1747 rows, 16 K/V heads: 26 us against 33; 18 tokens of
+  // 128 heads over up to 2245 rows 30.5 against 33; 1500 and 700 cost other batches 3 and 7 %).
   const long long tiles = (long long)p.Hkv * max(p.s.B, (int)(((long long)p.s.T << p.g_log2) >> (kPair ? 8 : 7)));
   long long most = all;
-  if (all >= 48 * tiles) {
-    const int least = (int)sqrtf((float)all / (float)(12 * tiles));
+  if (all >= 48 * tiles || p.piece_rows > 0) {
+    const float share2 = (float)all * (1.0f / (float)(12 * tiles) + (float)p.piece_rows * (1.0f / 6000.0f));
+    const int least = max(1, (int)sqrtf(share2));
     most = (all + least - 1) / least;
   }
   const int n = most < n_workers ? (int)most : n_workers;
@@ -1048,9 +1052,12 @@ void box_layouts(int page, BoxLayout* k, BoxLayout* v) {
 }
 
 template <bool kPair>
-hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p, int sms,
+hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, Params p, int sms,
                      cudaStream_t stream) {
-  const int workers = kPair ? sms / 2 : sms;
+  const int workers = kPair ? sms / 2 : sms, blocks = 4 * sms;  // (of the merge)
+  const bool many_rows = (long long)p.s.T * p.Hq > blocks;
+  const long long rows = ((long long)p.s.T << p.g_log2) / p.s.B;
+  p.piece_rows = !many_rows ? 0 : (int)(rows < Shape<kPair>::kRows ? rows : Shape<kPair>::kRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPair ? 2 * workers : workers, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1064,9 +1071,8 @@ hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.attrs = attr;
   cfg.numAttrs = kPair ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
-  const int blocks = 4 * sms, few = (long long)p.s.T * p.Hq > blocks ? 32 : 8;
   return launch_after(combine_kernel, dim3(blocks), 32 * kCombineWarps, stream, p, workers, (int)Shape<kPair>::kRows,
-                      few);
+                      many_rows ? 32 : 8);
 }
 
 }  // namespace
