@@ -361,10 +361,30 @@ __device__ __forceinline__ void find_start(const Params& p, int tq_log2, int wor
   });
 }
 
-__device__ __forceinline__ void store_32(void* dst, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void store_32(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// Lanes 4 q .. 4 q + 3 hold four rows of 32 columns; afterwards lane 4 q + i holds columns 8 i .. 8 i + 7 of
+// all four, row k in v[8 k .. 8 k + 7].
+__device__ __forceinline__ void transpose_4(uint32_t (&v)[32], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & bit) continue;
+      const int b = a | bit;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[8 * a + y] : v[8 * b + y], bit);
+        if (up) v[8 * a + y] = got;
+        else v[8 * b + y] = got;
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -769,32 +789,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_half32<128>(t_lanes + c0 * 32, o[0]);
           tmem_ld_half32<128>(t_lanes + c0 * 32 + 32, o[1]);
           tmem_wait_ld_regs2(o[0], o[1]);
-          // whole 32-byte sectors per thread: half of one, as 16-byte stores write them, costs as much
-          if (valid && whole) {
-            uint16_t* dst = p.O + orow * kMlaD + hf * 128 + c0 * 32;
+          // Four lanes exchange their 32-byte pieces, so that each store fills lines of 128 bytes (18 tokens of
+          // 128 heads over up to 2245 rows 26.8 us against 30.8, two short conversations 14.4 against 16.4).
+          const int n_valid = (w.q.n - w.first_token()) << p.g_log2, row4 = row & ~3, quarter = lane & 3;
+          if (whole) {
+            uint32_t v[32];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t v[8];
+            for (int y = 0; y < 32; ++y) {
+              const uint32_t* q = &o[y >> 4][2 * (y & 15)];
+              v[y] = pack_bf16x2(__uint_as_float(q[0]) * inv, __uint_as_float(q[1]) * inv);
+            }
+            transpose_4(v, lane);
 #pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                const uint32_t* q = &o[x >> 1][16 * (x & 1) + 2 * y];
-                v[y] = pack_bf16x2(__uint_as_float(q[0]) * inv, __uint_as_float(q[1]) * inv);
-              }
+            for (int k = 0; k < 4; ++k) {
+              const int r = row4 + k;
+              if (r >= n_valid) break;
+              const size_t at = (size_t)(w.q.q0 + w.first_token() + (r >> p.g_log2)) * p.Hq + (w.h << p.g_log2) +
+                                (r & ((1 << p.g_log2) - 1));
+              uint16_t* dst = p.O + at * kMlaD + hf * 128 + c0 * 32 + 16 * quarter;
               if (p.wide_stores) {
-                store_32(dst + 16 * x, v);
+                store_32(dst, &v[8 * k]);
               } else {
-                reinterpret_cast<uint4*>(dst + 16 * x)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<uint4*>(dst + 16 * x)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3]);
+                reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]);
               }
             }
-          } else if (valid) {
-            float* dst = p.ws_O + ((size_t)slot * Sh::kRows + row) * kMlaD + hf * 128 + c0 * 32;
+          } else {
+            float* dst = p.ws_O + ((size_t)slot * Sh::kRows + row4) * kMlaD + hf * 128 + c0 * 32 + 8 * quarter;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              uint32_t v[8];
+            for (int x = 0; x < 2; ++x) {
+              transpose_4(o[x], lane);
 #pragma unroll
-              for (int y = 0; y < 8; ++y) v[y] = o[x >> 2][8 * (x & 3) + y];
-              store_32(dst + 8 * x, v);
+              for (int k = 0; k < 4; ++k)
+                if (row4 + k < n_valid) store_32(dst + k * kMlaD + 32 * x, &o[x][8 * k]);
             }
           }
           __syncwarp();
