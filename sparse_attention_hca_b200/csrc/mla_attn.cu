@@ -30,7 +30,7 @@
 //
 // Measured (B200, 64 heads on one K/V head): 2048 tokens over 32768 rows 2.8 ms in a short run
 // (1.52 PFLOP/s), 2.95 ms when repeated (1.44 PFLOP/s; the power limit holds the clock at 1.45 GHz).
-// A product takes about 2320 cycles of 2048 for its MMAs (the tensor pipe is busy 88 % of the active
+// A product takes about 2300 cycles of 2048 for its MMAs (the tensor pipe is busy 89 % of the active
 // cycles): the S MMAs read A and B from shared memory at 128 bytes per cycle, its limit, next to the
 // incoming tiles.  32 sequences of 1K-32K rows, one token each: 106 us on the device, 5.4 TB/s (113
 // repeated).
@@ -152,9 +152,9 @@ struct SeqTiles {
   }
 };
 
-// A pair's row tile costs its output (4-5 us) besides its products (1.3 us each), so in lists that give
+// A pair's row tile costs its output (3-4 us) besides its products (1.3 us each), so in lists that give
 // every pair 2 products or more a tile weighs as much as this many more, which come first in it.  (3
-// sequences of 844 tokens over up to 1749 rows next to 26 single tokens, 16 heads: 57 us against 84; 361
+// sequences of 844 tokens over up to 1749 rows next to 26 single tokens, 16 heads: 59 us against 84; 361
 // tokens over 10164 rows, 16 heads, 61 against 62; 512 tokens from nothing, 64 heads, 33 against 37; a
 // weight of 2 is 2-4 % slower in the first two, 6 10 %.)  Not the tile of a
 // sequence with at most 32 rows to write (weighed as well, 2 chunks next to 22 single tokens of 8 rows took
