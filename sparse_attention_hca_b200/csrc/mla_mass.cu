@@ -18,7 +18,7 @@
 //
 // Schedule: as the attention kernel's, one list of (256-row block, 128-row Q tile) products over the
 // batch -- sequence, K/V head, block, Q tile, those that see some row of the block -- cut evenly over
-// the pairs.  A block that several pairs share leaves partial sums in the workspace, which
+// the pairs (see kBlockCost).  A block that several pairs share leaves partial sums in the workspace, which
 // add_kernel adds up in list order; every row's mass gets exactly one addition per call.
 //
 // Measured (B200, 64 heads on one K/V head): 1021 tokens over 16381 rows 380 us in a short run (1.40
@@ -63,6 +63,11 @@ struct __align__(8) Barriers {
 
 // ------------------------------------------------------------------ the list of products
 
+// A block's K tile takes as long to arrive as about one more product, so a block takes one place in the
+// list besides its products; the place comes first.  (3 chunks of 435 tokens over 1.3K-4.8K rows next to 22
+// single tokens, whose blocks are one product each: 113 us against 153; two of 433 next to 21, 128 heads, 55 against 73.)
+constexpr int kBlockCost = 1;
+
 // One sequence's part of the list (of one K/V head).
 struct SeqBlocks {
   int base, n, len, s_log2;  // s_log2: tokens of a Q tile
@@ -83,11 +88,13 @@ struct SeqBlocks {
     const long long c = k - kf, sum = ((long long)kf + k - 1) * c / 2;
     return kf * q + c * (q + cb) - (sum << (8 - s_log2));
   }
+  // where block k begins in the list
+  __host__ __device__ long long start(int k) const { return before(k) + (long long)k * kBlockCost; }
   __host__ __device__ int find(long long w) const {
     int lo = 0, hi = blocks();
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (before(mid) <= w) lo = mid;
+      if (start(mid) <= w) lo = mid;
       else hi = mid;
     }
     return lo;
@@ -96,7 +103,7 @@ struct SeqBlocks {
 
 struct Start {
   long long count;
-  int b, h, k, t;
+  int b, h, k, at;  // where it begins: `at` places into block k
   PagedSeq q;  // sequence b
 };
 
@@ -104,7 +111,7 @@ struct Start {
 struct Walk {
   const Params& p;
   long long left;
-  int b, h, k, t0, t1, first, last;  // Q tiles [t0, t1) of the block's [first, last)
+  int b, h, k, at, t0, t1, first, last;  // Q tiles [t0, t1) of the block's [first, last)
   PagedSeq q;
   SeqBlocks s;
   __device__ Walk(const Params& p_, const Start& st) : p(p_) {
@@ -114,17 +121,17 @@ struct Walk {
     k = st.k;
     if (left > 0) {
       load(st.q);
-      cut(st.t);
+      cut(st.at);
     }
   }
   __device__ bool done() const { return left <= 0; }
   __device__ bool whole() const { return t0 == first && t1 == last; }
   // whether the product after this piece's last one uses the same Q tile
   __device__ bool same_tile_next() const {
-    return left > t1 - t0 && t1 == last && k + 1 < s.blocks() && s.first_tile(k + 1) == last - 1;
+    return left - places() > kBlockCost && t1 == last && k + 1 < s.blocks() && s.first_tile(k + 1) == last - 1;
   }
   __device__ void next() {
-    left -= t1 - t0;
+    left -= places();
     if (left <= 0) return;
     if (++k == s.blocks()) {
       k = 0;
@@ -139,7 +146,7 @@ struct Walk {
         } while (s.blocks() == 0);
       }
     }
-    cut(s.first_tile(k));
+    cut(0);
   }
 
  private:
@@ -150,12 +157,15 @@ struct Walk {
     s.len = q.len;
     s.s_log2 = 7 - p.g_log2;
   }
-  __device__ void cut(int t) {
-    t0 = t;
+  __device__ int places() const { return t1 - first + kBlockCost - at; }  // this piece's part of the share
+  __device__ void cut(int from) {  // places [0, kBlockCost) of a block hold no product
+    at = from;
     first = s.first_tile(k);
     last = s.q_tiles();
-    const long long e = (long long)t0 + left;
+    t0 = first + (at > kBlockCost ? at - kBlockCost : 0);
+    const long long e = first + at + left - kBlockCost;
     t1 = e < last ? (int)e : last;
+    if (t1 <= t0) left = 0;  // the share ends before the block's first product
   }
 };
 
@@ -174,7 +184,7 @@ __device__ __forceinline__ void find_start(const Params& p, int worker, int n_wo
   auto work_of = [&](int b, bool report) -> long long {
     if (b >= p.s.B) return 0;
     const SeqBlocks s = blocks_of(paged_seq(p.s, b, report));
-    return s.before(s.blocks()) * p.Hkv;
+    return s.start(s.blocks()) * p.Hkv;
   };
   auto scan = [&](long long x, long long& total) -> long long {  // inclusive prefix over the threads
 #pragma unroll
@@ -209,7 +219,7 @@ __device__ __forceinline__ void find_start(const Params& p, int worker, int n_wo
     out->h = (int)(r / per_head);
     const long long in = r - out->h * per_head;
     out->k = s.find(in);
-    out->t = s.first_tile(out->k) + (int)(in - s.before(out->k));
+    out->at = (int)(in - s.start(out->k));
   };
   if (p.s.B <= kThreads) {  // known from the first pass
     find(tid, mine_to - mine, mine_to);
@@ -418,10 +428,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int c_hi = min(kCols, n_rows - t * kCols);                                // uniform
         const int c_lo = max(0, min(kCols, lo_row - t * kCols));                              // this row's
         const bool all = c_hi == kCols && __all_sync(0xffffffffu, c_lo == 0);
+        const int c_end = __all_sync(0xffffffffu, c_lo >= c_hi) ? 0 : c_hi;  // 0: no row of the warp is seen
         float a4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          if (c * 32 >= c_hi) break;
+          if (c * 32 >= c_end) break;
           uint32_t v[32];
           tmem_ld32_nowait(t_lanes + sb * kCols + c * 32, v);
           tmem_wait_ld_regs(v);
@@ -616,7 +627,7 @@ extern "C" hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_r
   {
     const uint64_t dims[5] = {64, (uint64_t)page, kMlaD / 64, (uint64_t)Hkv, (uint64_t)n_pages};
     const uint64_t strides[4] = {(uint64_t)Hkv * kMlaD * 2, 64 * 2, (uint64_t)kMlaD * 2, (uint64_t)k_page_stride * 2};
-    const uint32_t box[5] = {64, 1u << p.box_log2, groups ? kMlaD / 64 : 1, 1, 1};
+    const uint32_t box[5] = {64, 1u << p.box_log2, groups ? kMlaD / 64u : 1u, 1, 1};
     if (!encode_tmap_bf16(&mk, 5, const_cast<hcadsa_bf16*>(K_pool), dims, strides, box, true)) return HCADSA_ERR_CUDA;
   }
   mass_kernel<<<2 * pairs, kThreads, kSmemBytes, as_stream(stream)>>>(mq, mk, p);
