@@ -866,8 +866,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Every block lists the row tiles to merge from the workers' records and takes its share of the work
 // items: with up to `few` pieces an item is 8 rows, one warp each; with more (a long cache cut over
 // many workers) it is one row, whose pieces the 8 warps divide among themselves and add up through
-// shared memory, in warp order.  `few` is 8, or 32 where there are more rows than blocks, which one
-// warp per row keeps busy (124 tokens over 1747 rows, 16 K/V heads: 33.5 us against 43).  Lane l holds
+// shared memory, in warp order.  `few` is 8, or 32 where there are twice as many rows as blocks,
+// which one warp per row keeps busy (124 tokens over 1747 rows, 16 K/V heads: 33.5 us against 43; but 5
+// tokens of 128 heads over up to 7209 rows 31.7 against 28.7, with 640 rows for 592 blocks).  Lane l holds
 // columns 8 l .. 8 l + 7; the lanes read the pieces' (max, sum) side by side, so the loads of the rows
 // do not wait on one another.
 // (One sequence of 32768 rows cut into 148 pieces of 64 rows: one warp per row took 30 us of the call's 47.)
@@ -1082,9 +1083,9 @@ template <bool kPair>
 hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, Params p, int sms,
                      cudaStream_t stream) {
   const int workers = kPair ? sms / 2 : sms, blocks = 4 * sms;  // (of the merge)
-  const bool many_rows = (long long)p.s.T * p.Hq > blocks;
+  const long long all_rows = (long long)p.s.T * p.Hq;
   const long long rows = ((long long)p.s.T << p.g_log2) / p.s.B;
-  p.piece_rows = !many_rows ? 0 : (int)(rows < Shape<kPair>::kRows ? rows : Shape<kPair>::kRows);
+  p.piece_rows = all_rows <= blocks ? 0 : (int)(rows < Shape<kPair>::kRows ? rows : Shape<kPair>::kRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPair ? 2 * workers : workers, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1099,7 +1100,7 @@ hcadsa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.numAttrs = kPair ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, attn_kernel<kPair>, mq, mk, mv, p) != cudaSuccess) return launch_status();
   return launch_after(combine_kernel, dim3(blocks), 32 * kCombineWarps, stream, p, workers, (int)Shape<kPair>::kRows,
-                      many_rows ? 32 : 8);
+                      all_rows > 2 * blocks ? 32 : 8);
 }
 
 }  // namespace

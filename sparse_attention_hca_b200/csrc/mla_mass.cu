@@ -65,7 +65,8 @@ struct __align__(8) Barriers {
 
 // A block's K tile takes as long to arrive as about one more product, so a block takes one place in the
 // list besides its products; the place comes first.  (3 chunks of 435 tokens over 1.3K-4.8K rows next to 22
-// single tokens, whose blocks are one product each: 113 us against 153; two of 433 next to 21, 128 heads, 55 against 73.)
+// single tokens, whose blocks are one product each: 113 us against 153; two of 433 next to 21, 128 heads,
+// 55 against 73.)
 constexpr int kBlockCost = 1;
 
 // One sequence's part of the list (of one K/V head).
