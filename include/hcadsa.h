@@ -342,8 +342,8 @@ hcadsa_status attn_gate_vha_fwd(const hcadsa_bf16* O, const hcadsa_bf16* cq, con
  *   table   : [B, max_pages] int32; row i of sequence b's cache lies in page
  *              table[b][i / page] at place i % page
  *   cu_q    : [B + 1] int32, ascending; sequence b's new tokens are the packed rows cu_q[b] ..
- *              cu_q[b+1]-1 (none, one, or a chunk).  Packed rows behind cu_q[B] are neither read nor
- *              written.
+ *              cu_q[b+1]-1 (none, one, or a chunk).  Packed rows behind cu_q[B] do not matter and
+ *              are not written.
  *   kv_len  : [B] int32, rows in b's cache, its new tokens included
  *   seen    : [B] int32, tokens the sequence has had, the new ones included (kv_len plus what was
  *              evicted); NULL: kv_len
@@ -351,16 +351,19 @@ hcadsa_status attn_gate_vha_fwd(const hcadsa_bf16* O, const hcadsa_bf16* cq, con
  *              pool row
  * page is a power of two, 16 to 1024; d == 256; Hq / Hkv a power of two up to 128; the attention calls
  * take up to 2^23 new tokens (HCADSA_ERR_UNSUPPORTED otherwise).  table, cu_q, kv_len, seen, pos and
- * mass need 4-byte alignment (moves: 8), the bf16 tensors 16.  The lengths and tables are device data: a value out of range (a page that
- * is not in the pool, a length beyond max_pages * page, cu_q out of order) is recorded as
- * HCADSA_ERR_DEVICE_BOUNDS, and the rows it concerns are skipped or read as zeros; nothing outside
- * the tensors is touched.
+ * mass need 4-byte alignment (moves: 8), the bf16 tensors 16.  The lengths and tables are device data:
+ * a value out of range (a page that is not in the pool, a length beyond max_pages * page, cu_q out of
+ * order or beyond the packed rows) is recorded as HCADSA_ERR_DEVICE_BOUNDS, and nothing outside the
+ * tensors is touched.  Rows of a page that is not in the pool are read as zeros and not written; a
+ * length or an entry of cu_q out of range counts as the nearest one in range, except that
+ * mla_cache_append never writes a row anywhere but at its own place.
  */
 
 /*
  * Writes a chunk's new rows to the ends of their sequences' caches: packed row cu_q[b] + i becomes
  * row kv_len[b] - n_b + i of sequence b (n_b its new tokens), with pos = seen[b] - n_b + i and
- * mass = 0.
+ * mass = 0.  A row without a place (before row 0, or behind the sequence's last page) is skipped and
+ * recorded.
  *   K, V : [T, Hkv, 256] bf16, consecutive tokens k_row_stride / v_row_stride elements apart (a
  *          multiple of 8, at least Hkv * 256: slices of a fused projection are fine)
  *   pos, mass : written for the new rows; either may be NULL

@@ -64,14 +64,19 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const AppendParams 
     const int b = owner[threadIdx.x];
     int pg = -1, r = 0;
     if (b >= 0) {  // otherwise a packed row behind the last sequence
-      const PagedSeq q = paged_seq(p.s, b, false);
-      const int back = q.q0 + q.n - (t0 + (int)threadIdx.x);  // rows from this one to the end
-      r = q.len - back;
-      if (r >= 0) pg = paged_page(p.s, b, r);
-      else raise_device_error(p.s.err, kErrDeviceBounds);  // the cache is declared shorter than the chunk
+      // from the declared end, not the clamped one: a row without a place in the table may not take
+      // the place of another
+      const long long back = (long long)p.s.cu_q[b + 1] - (t0 + (int)threadIdx.x);  // rows from this one to the end
+      const long long at = p.s.kv_len[b] - back;
+      if (at >= 0 && at < (long long)p.s.max_pages << p.s.page_log2) {
+        r = (int)at;
+        pg = paged_page(p.s, b, r);
+      } else {
+        raise_device_error(p.s.err, kErrDeviceBounds);
+      }
       if (pg >= 0) {
         const size_t slot = (((size_t)pg << p.s.page_log2) + (r & page_mask)) * p.Hkv;
-        const int ps = p.seen ? p.seen[b] - back : r;
+        const int ps = p.seen ? (int)(p.seen[b] - back) : r;
         for (int h = 0; h < p.Hkv; ++h) {
           if (p.pos) p.pos[slot + h] = ps;
           if (p.mass) p.mass[slot + h] = 0.0f;
