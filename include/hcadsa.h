@@ -382,7 +382,8 @@ hcadsa_status mla_cache_append(const hcadsa_bf16* K, const hcadsa_bf16* V, long 
  * Query head h reads K/V head h / (Hq/Hkv).  A token that sees no row (kv_len[b] < n_b) gets O = 0,
  * lse = -inf.  What lies in a page behind the last row of its sequence does not matter (NaN
  * included); the rows of the sequence itself should be finite, since a NaN or infinity in V also
- * reaches the tokens that do not see its row but share a tile of 128 rows with it.
+ * reaches the tokens that do not see its row but share a tile of 128 rows with it.  A NaN among the
+ * scores a (token, head) row sees, from Q or K, is a NaN in that row's O and lse, and in no other.
  *   Q   : [T, Hq, 256] bf16, tokens q_row_stride elements apart (a multiple of 8)
  *   O   : [T, Hq, 256] bf16 (written for the tokens of the batch; not over an input); lse: [T, Hq]
  *         fp32 or NULL

@@ -773,11 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp_valid) {
         const float l = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
         const size_t orow = (size_t)(w.q.q0 + tok) * p.Hq + (w.h << p.g_log2) + my_head;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;  // (a NaN stays one: O and lse show it)
         const int slot = 2 * worker + (w.j0 == 0 ? 1 : 0);
         if (valid && hf == 0) {
           if (whole) {
-            if (p.lse) p.lse[orow] = l > 0.0f ? (m_run + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            if (p.lse) p.lse[orow] = l != 0.0f ? (m_run + __log2f(l)) * 0.69314718055994531f : -INFINITY;
           } else {
             p.ws_ml[(size_t)slot * 2 * Sh::kRows + row] = m_run;
             p.ws_ml[(size_t)slot * 2 * Sh::kRows + Sh::kRows + row] = l;
@@ -863,6 +863,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // c+1, c+2, ... (piece k >= 1 is the one worker c + k began with), in that order: with M the largest
 // of the maxima,
 //     O = sum_k 2^(m_k - M) O_k / sum_k 2^(m_k - M) l_k.
+// A piece that sees no row has l_k = 0 and no weight; one with a NaN among its scores has l_k = NaN, which
+// reaches the row's O and lse through the denominator.
 // Every block lists the row tiles to merge from the workers' records and takes its share of the work
 // items: with up to `few` pieces an item is 8 rows, one warp each; with more (a long cache cut over
 // many workers) it is one row, whose pieces the 8 warps divide among themselves and add up through
@@ -966,10 +968,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4)
         m = ml[0];
         l = ml[n_rows];
       }
-      M = l > 0.0f ? m : -INFINITY;
+      M = l != 0.0f ? m : -INFINITY;
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float w_mine = l > 0.0f ? exp2f(m - M) : 0.0f;
+      const float w_mine = l != 0.0f ? exp2f(m - M) : 0.0f;
       den = 0.0f;
 #pragma unroll 4
       for (int k = 0; k < n; ++k) {
@@ -986,7 +988,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4)
         m = ml[0];
         l = ml[n_rows];
       }
-      M = l > 0.0f ? m : -INFINITY;
+      M = l != 0.0f ? m : -INFINITY;
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       __syncthreads();  // the item before has been read
@@ -994,7 +996,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4)
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, red[0][w]);
-      const float w_mine = l > 0.0f ? exp2f(m - M) : 0.0f;
+      const float w_mine = l != 0.0f ? exp2f(m - M) : 0.0f;
       if (tid < n) weight[tid] = w_mine;
       den = w_mine * l;
 #pragma unroll
@@ -1018,7 +1020,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4)
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] += part[w][lane * 8 + x];
     }
-    const float inv = den > 0.0f ? 1.0f / den : 0.0f;
+    const float inv = den != 0.0f ? 1.0f / den : 0.0f;
     const size_t orow = (size_t)(tile.x + tok) * p.Hq + (tile.z << p.g_log2) + (row & ((1 << p.g_log2) - 1));
     uint4 v;
     v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
@@ -1026,7 +1028,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 4)
     v.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
     v.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
     reinterpret_cast<uint4*>(p.O + orow * kMlaD)[lane] = v;
-    if (p.lse && lane == 0) p.lse[orow] = den > 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
+    if (p.lse && lane == 0) p.lse[orow] = den != 0.0f ? (M + __log2f(den)) * 0.69314718055994531f : -INFINITY;
   }
 }
 

@@ -1,4 +1,6 @@
 """GPU tests of the paged cache of the full-context (MLA) layers in a server's use, and of what its inputs may get wrong."""
+import math
+
 import pytest
 import torch
 from test_gpu_mla_paged import D, Cache, hd, i32  # noqa: F401  (hd: a fixture)
@@ -65,3 +67,49 @@ def test_append_of_a_cut_batch(hd):  # noqa: F811
     expect_bounds_error(hd)
     for got, ref in zip((c.K, c.V, pos), want):
         assert same(got, ref)
+
+
+# ----------------------------------------------------------------------------- values that are not finite
+
+FINITE = {
+    "one_tile": dict(q_len=[1], kv_len=[40]),
+    "few_pieces": dict(q_len=[1, 1], kv_len=[40, 300]),
+    "many_pieces": dict(q_len=[1], kv_len=[40000]),
+    "prompt": dict(q_len=[300], kv_len=[300], page=16),
+    "whole_row_tiles": dict(q_len=[256], kv_len=[1024]),
+    "chunk_pieces": dict(q_len=[70, 1], kv_len=[5000, 900], Hq=16, Hkv=2, page=32),
+}
+
+
+@pytest.mark.parametrize("where", ["Q", "K"])
+@pytest.mark.parametrize("name", list(FINITE))
+def test_nan_stays_visible(hd, name, where):  # noqa: F811
+    """A NaN in a query, or in a cached row that a token sees, is a NaN in that token's O, lse and weights, whether
+    or not its row tile was cut into pieces; nothing else changes."""
+    c = Cache(seed=3, **FINITE[name])
+    T, grp = c.q.shape[0], c.Hq // c.Hkv
+    O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+    mass = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse)
+    bad = torch.zeros((T, c.Hq), dtype=torch.bool, device="cuda")
+    bad_row = torch.zeros(mass.shape, dtype=torch.bool, device="cuda")
+    t0 = 0
+    for b, n in enumerate(c.q_len):
+        if where == "Q":
+            for i, h in ((n - 1, 0), (n // 2, c.Hq - 1)):
+                c.q[t0 + i, h, 5] = math.nan
+                bad[t0 + i, h] = True
+                at = places(c, b, list(range(c.kv[b] - n + i + 1)))
+                bad_row[at[0], at[1], h // grp] = True
+        else:
+            row, kvh = c.kv[b] - (n + 1) // 2, c.Hkv - 1  # the last half of the tokens see it
+            c.K[places(c, b, [row])[0], row % c.page, kvh, 200] = math.nan
+            first = row - (c.kv[b] - n)
+            bad[t0 + first : t0 + n, kvh * grp :] = True
+            bad_row[c.rows(b)[0], c.rows(b)[1], kvh] = True
+        t0 += n
+    O2, lse2 = hd.mla_paged_attn_fwd(c.q, *c.args(), return_lse=True)
+    mass2 = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse2)
+    hd.hcadsa_check_device_error()
+    assert torch.isnan(O2[bad]).all() and torch.isnan(lse2[bad]).all()
+    assert same(O2[~bad], O[~bad]) and same(lse2[~bad], lse[~bad])
+    assert torch.isnan(mass2[bad_row]).all() and same(mass2[~bad_row], mass[~bad_row])
