@@ -588,11 +588,23 @@ def _need_pools(K_pool, V_pool):
     return n_pages, page, Hkv, d, k_page, _need_pool(V_pool, "V_pool", K_pool.shape)[4]
 
 
+_I32_MAX = 2**31 - 1
+
+
+def _need_i32(**counts):
+    """Counts and sizes are C ints, which ctypes fills modulo 2^32."""
+    for name, x in counts.items():
+        if not -_I32_MAX <= x <= _I32_MAX:
+            raise ValueError(f"{name} = {x} does not fit a 32-bit integer")
+
+
 def _need_batch(table, kv_len, cu_q=None, seen=None):
     shape = table.shape
     if len(shape) != 2:
         raise ValueError(f"table has shape {tuple(shape)}, expected [B, max_pages]")
     B, max_pages = shape
+    if B > _I32_MAX or max_pages > _I32_MAX:
+        _need_i32(B=B, max_pages=max_pages)
     i32 = torch.int32
     # checked in place: these run once per call of a decode step
     if not (table.dtype is i32 and table.is_contiguous() and kv_len.dtype is i32 and kv_len.shape == (B,) and
@@ -739,6 +751,7 @@ def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int
     n_pages, page, Hkv = shape = mass.shape
     _need_slots(pos, mass, shape)
     B, max_pages = _need_batch(table, kv_len, seen=seen)
+    _need_i32(budget=budget, n_sink=n_sink, n_recent=n_recent)
     n = max(0, min(budget, max_pages * page - budget))
     if moves is not None:
         _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
@@ -767,9 +780,11 @@ def mla_cache_move(moves, K_pool, V_pool, table, *, pos=None, mass=None, stream=
         raise ValueError(f"table has shape {tuple(table.shape)}, expected [B, max_pages]")
     B, max_pages = table.shape
     _need(table, torch.int32, "table")
+    _need_i32(B=B, max_pages=max_pages)
     if moves.dim() != 4:
         raise ValueError(f"moves has shape {tuple(moves.shape)}, expected [{B}, {Hkv}, n, 2]")
     n = moves.shape[2]
+    _need_i32(n_moves=n)
     _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
     _need_slots(pos, mass, (n_pages, page, Hkv))
     _, raw = _device_and_stream(stream, moves, table, K_pool, V_pool, pos, mass)

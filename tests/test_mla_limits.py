@@ -1,0 +1,34 @@
+"""Further refusals of the paged-cache calls of the full-context (MLA) layers, without a GPU."""
+import pytest
+import torch
+from test_mla_checks import _tensors, i32
+
+import sparse_attention_hca_b200 as hd
+
+
+@pytest.mark.parametrize("kw", [dict(n_recent=2 ** 32), dict(n_sink=2 ** 32), dict(n_recent=2 ** 31), dict(n_sink=-(2 ** 32)),
+                                dict(n_recent=-(2 ** 31) - 1), dict(budget=2 ** 32 + 100), dict(budget=-(2 ** 32) + 100),
+                                dict(budget=2 ** 64 + 100)])
+def test_select_counts_beyond_32_bits(kw):
+    """Counts are C ints: one that does not fit is refused, not taken modulo 2^32."""
+    t = _tensors()
+    kw = dict(dict(budget=100, n_sink=4, n_recent=50), **kw)
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_evict_select(t["mass"], t["pos"], t["table"], t["kv"], None, kw.pop("budget"), **kw)
+
+
+def test_sizes_beyond_32_bits():
+    """Nor do sizes of tensors wrap: a table or a list of moves as wide as 2^32, or as many sequences."""
+    t = _tensors()
+    wide = torch.empty(2, 2 ** 32 + 3, dtype=i32, device="meta")
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_paged_attn_fwd(t["q"], t["K"], t["V"], wide, t["cu"], t["kv"])
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_paged_attn_mass(t["q"], t["K"], torch.empty(2 ** 32 + 2, 3, dtype=i32, device="meta"), t["cu"], t["kv"],
+                               t["lse"])
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_evict_select(t["mass"], t["pos"], wide, t["kv"], None, 100)
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_cache_move(t["moves"], t["K"], t["V"], wide)
+    with pytest.raises(ValueError, match="32-bit"):
+        hd.mla_cache_move(torch.empty(2, 1, 2 ** 32 + 5, 2, dtype=i32, device="meta"), t["K"], t["V"], t["table"])
