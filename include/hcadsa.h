@@ -422,7 +422,8 @@ hcadsa_status mla_paged_attn_mass(const hcadsa_bf16* Q, long long q_row_stride, 
  * keep their place; entry i of
  *   moves   : [B, Hkv, n_moves, 2] int32 (written): the i-th staying row >= budget and the i-th freed
  *             row < budget, both ascending; entries past the last move are (-1, -1)
- *   new_len : [B] int32 (written, not the kv_len array): min(kv_len, budget)
+ *   new_len : [B] int32 (written; apart from kv_len and seen, HCADSA_ERR_SHAPE otherwise):
+ *             min(kv_len, budget)
  * A cache of at most `budget` rows gets no moves.  Nothing else is written: mla_cache_move makes
  * the moves.  budget >= 1, 0 <= n_sink, 0 <= n_recent, n_sink + n_recent <= budget, n_moves at
  * least min(budget, max_pages * page - budget) (HCADSA_ERR_SHAPE otherwise).

@@ -757,8 +757,9 @@ def mla_evict_select(mass, pos, table, kv_len, seen, budget: int, *, n_sink: int
         _need_exact(moves, torch.int32, "moves", (B, Hkv, n, 2))
     if new_len is not None:
         _need_exact(new_len, torch.int32, "new_len", (B,))
-        if new_len.data_ptr() == kv_len.data_ptr():
-            raise ValueError("new_len must not be kv_len: kv_len is read while new_len is written")
+        for name, x in (("kv_len", kv_len), ("seen", seen)):
+            if x is not None and abs(new_len.data_ptr() - x.data_ptr()) < 4 * B:
+                raise ValueError(f"new_len must not be {name}, nor overlap it: it is read while new_len is written")
     _, raw = _device_and_stream(stream, mass, pos, table, kv_len, seen, moves, new_len)
     if moves is None:
         moves = _empty(mass, (B, Hkv, n, 2), torch.int32, stream)

@@ -413,6 +413,12 @@ extern "C" hcadsa_status mla_evict_select(const float* mass, const int32_t* pos,
   if (!aligned4(mass) || !aligned4(pos) || !aligned4(table) || !aligned4(kv_len) || !aligned4(seen) ||
       (reinterpret_cast<uintptr_t>(moves) & 7u) || !aligned4(new_len))
     return HCADSA_ERR_ALIGN;
+  // new_len is written by one CTA of a sequence while others still read its lengths
+  const auto overlap = [&](const int32_t* x) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), n = reinterpret_cast<uintptr_t>(new_len);
+    return x && (a < n ? n - a : a - n) < 4 * (uintptr_t)B;
+  };
+  if (overlap(kv_len) || overlap(seen)) return HCADSA_ERR_SHAPE;
   if (B == 0) return HCADSA_OK;
   const Device dev = this_device();
   if (dev.sms <= 0) return HCADSA_ERR_CUDA;

@@ -1,7 +1,7 @@
 """Further refusals of the paged-cache calls of the full-context (MLA) layers, without a GPU."""
 import pytest
 import torch
-from test_mla_checks import _tensors, i32
+from test_mla_checks import F, SELECT, _tensors, i32, lib  # noqa: F401  (lib: a fixture)
 
 import sparse_attention_hca_b200 as hd
 
@@ -32,3 +32,24 @@ def test_sizes_beyond_32_bits():
         hd.mla_cache_move(t["moves"], t["K"], t["V"], wide)
     with pytest.raises(ValueError, match="32-bit"):
         hd.mla_cache_move(torch.empty(2, 1, 2 ** 32 + 5, 2, dtype=i32, device="meta"), t["K"], t["V"], t["table"])
+
+
+def test_select_lengths_may_not_overlap():
+    """new_len is written while other lists still read kv_len and seen."""
+    t = _tensors(B=3)
+    buf = torch.zeros(8, dtype=i32)
+    for kv, seen, new in ((buf[0:3], None, buf[0:3]), (buf[0:3], None, buf[2:5]), (buf[2:5], None, buf[0:3]),
+                          (buf[0:3], buf[3:6], buf[3:6]), (buf[0:3], buf[3:6], buf[5:8])):
+        with pytest.raises(ValueError, match="new_len must not"):
+            hd.mla_evict_select(t["mass"], t["pos"], t["table"], kv, seen, 100, new_len=new)
+    with pytest.raises(ValueError, match="CUDA"):  # side by side is fine; nothing lies on a GPU
+        hd.mla_evict_select(t["mass"], t["pos"], t["table"], buf[0:3], None, 100, new_len=buf[3:6])
+
+
+def test_select_lengths_may_not_overlap_in_c(lib):  # noqa: F811
+    def call(**kw):
+        return lib.mla_evict_select(*dict(SELECT, moves=2 * F, **kw).values())
+
+    assert call(kv=F, new=F) == -2 and call(kv=F, new=F + 4) == -2 and call(kv=F + 4, new=F) == -2
+    assert call(kv=F, seen=F + 64, new=F + 64) == -2 and call(kv=F, seen=F + 64, new=F + 68) == -2
+    assert call(kv=F, seen=F, new=F + 8, B=0) == 0
