@@ -254,11 +254,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();  // 0: the leader, which issues the MMAs
   const int worker = (int)blockIdx.x >> 1, n_workers = (int)gridDim.x >> 1;
-  // the tiles need every byte there is, so their 1024-byte alignment is the declaration's
-  if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) raise_device_error(p.s.err, kErrDeviceBounds);
-    return;
-  }
   uint8_t* sK = smem;
   uint8_t* sQ = smem + 2 * kKBytes;
   if (threadIdx.x == 0) {
@@ -287,6 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   cluster_arrive();
   find_start(p, worker, n_workers, &start);
+  // the tiles need every byte there is, so their 1024-byte alignment is the declaration's; placed
+  // elsewhere, no pair takes any work, and all record that
+  if (threadIdx.x == 0 && (smem_u32(smem) & 1023u)) {
+    raise_device_error(p.s.err, HCADSA_ERR_CUDA);
+    start.count = 0;
+  }
   tc_fence_before();
   __syncthreads();
   cluster_wait();  // barriers and TMEM of both CTAs exist before any cross-CTA operation

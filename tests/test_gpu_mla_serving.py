@@ -113,3 +113,26 @@ def test_nan_stays_visible(hd, name, where):  # noqa: F811
     assert torch.isnan(O2[bad]).all() and torch.isnan(lse2[bad]).all()
     assert same(O2[~bad], O[~bad]) and same(lse2[~bad], lse[~bad])
     assert torch.isnan(mass2[bad_row]).all() and same(mass2[~bad_row], mass[~bad_row])
+
+
+# ----------------------------------------------------------------------------- scratch
+
+
+@pytest.mark.parametrize("fill", [0xff, 0x01, 0x00])
+def test_what_a_workspace_held_does_not_matter(hd, fill):  # noqa: F811
+    """Small batches leave most workers without work: their records have to be written too."""
+    for q_len, kv_len in (([1], [1]), ([1, 1], [300, 40]), ([70], [700]), ([0, 0], [5, 9])):
+        c = Cache(q_len, kv_len, Hq=16, seed=19)
+        T = max(1, sum(q_len))
+        if not sum(q_len):
+            c.q = c.rand(1, 16, D)
+        O, lse = hd.mla_paged_attn_fwd(c.q, *c.args(), O=torch.ones_like(c.q), lse=torch.ones(T, 16, device="cuda"),
+                                       return_lse=True)
+        mass = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse)
+        ws = [torch.full((getattr(hd.lib(), f + "_workspace_size")(len(q_len), T, 16, 1),), fill, dtype=torch.uint8,
+                         device="cuda") for f in ("mla_paged_attn_fwd", "mla_paged_attn_mass")]
+        O2, lse2 = hd.mla_paged_attn_fwd(c.q, *c.args(), O=torch.ones_like(c.q), lse=torch.ones(T, 16, device="cuda"),
+                                         return_lse=True, workspace=ws[0])
+        mass2 = hd.mla_paged_attn_mass(c.q, c.K, c.table, c.cu, c.kv_len, lse, workspace=ws[1])
+        hd.hcadsa_check_device_error()
+        assert same(O2, O) and same(lse2, lse) and same(mass2, mass)

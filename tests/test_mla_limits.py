@@ -1,4 +1,6 @@
 """Further refusals of the paged-cache calls of the full-context (MLA) layers, without a GPU."""
+import os
+
 import pytest
 import torch
 from test_mla_checks import F, SELECT, _tensors, i32, lib  # noqa: F401  (lib: a fixture)
@@ -53,3 +55,15 @@ def test_select_lengths_may_not_overlap_in_c(lib):  # noqa: F811
     assert call(kv=F, new=F) == -2 and call(kv=F, new=F + 4) == -2 and call(kv=F + 4, new=F) == -2
     assert call(kv=F, seen=F + 64, new=F + 64) == -2 and call(kv=F, seen=F + 64, new=F + 68) == -2
     assert call(kv=F, seen=F, new=F + 8, B=0) == 0
+
+
+@pytest.mark.parametrize("name", ["attn", "mass"])
+def test_no_way_out_before_the_records(name):
+    """The merging kernel that follows trusts every worker's record in the workspace, so the main kernel may not end
+    before it has written its own."""
+    with open(os.path.join(os.path.dirname(hd.__file__), "csrc", f"mla_{name}.cu")) as f:
+        text = f.read()
+    body = text[text.index(f"{name}_kernel(const __grid_constant__") :]
+    body = body[: body.index("launch_dependents();")]
+    assert "p.ws_meta + worker * kMetaInts" in body
+    assert "return;" not in body
