@@ -5,7 +5,7 @@
 // MLA layers keep every token's K and V.  A cache row is 256 bf16 per K/V head in each pool.
 //
 // Both kernels only copy 512-byte rows (one warp instruction: lane l moves bytes 16 l .. 16 l + 15),
-// so their bound is HBM: 2 KB of traffic per row pair and direction.  Measured (B200): 16384 tokens of
+// so their bound is HBM: 1 KB read and 1 KB written per pair of K and V rows.  Measured (B200): 16384 tokens of
 // 4 K/V heads appended in 27 us (5.0 TB/s of the 135 MB), 98284 moves in 41 us (5.0 TB/s); 4, 8 and
 // 16 moves per warp 43, 41 and 51 us; 4, 8 and 16 tokens per block 29, 27 and 29 us.
 #include "mla_host.h"

@@ -13,14 +13,15 @@
 //     in shared memory.  The budget-th largest key is found with a radix select of 11, 11 and 10
 //     bits: a histogram per CTA and pass, with one cluster barrier per pass.  One warp of every CTA
 //     then reads, through distributed shared memory, 64 sums of 32 bins from each CTA, and the 32
-//     bins of the group that holds the rank: all CTAs follow the same bin, and a pass moves 768
-//     words per CTA instead of whole histograms (8 x 2048 words took 9000 cycles).
+//     bins of the group that holds the rank: all CTAs follow the same bin.  The loops run to the largest
+//     cluster of the variant, so a pass reads 8 x 96 words (16 x 96 for clusters of 16) per CTA instead of
+//     whole histograms (8 x 2048 words took 9000 cycles).
 //   * Ties at the threshold are taken in row order: from counts per warp (a warp owns a contiguous run
 //     of its CTA's slice) and per CTA every row knows its rank.  No atomics decide anything that is
 //     written: the result does not depend on timing.
 //   * Entries are gathered in shared memory, 128 rows of a warp at a time, and written side by side.
-// What bounds it is latency: two dependent loads per row, three passes over the keys, four cluster
-// barriers.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
+// What bounds it is latency: two dependent loads per row, three passes over the keys with a
+// cluster barrier each, and two more for the counts and the end.  A thread takes four consecutive rows at a time (a page holds at least 16).  Slices that
 // do not fit in shared memory are read from global memory again in every pass.
 // Measured (B200): 32 lists of 4224 rows cut to 4096 in 12.4 us, 4 lists of 131072 cut to 32768 in 23.
 #include <mutex>
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 4 : 1) select_kern
     return;
   }
   // CTAs [0, c1) share the rows [0, budget), the others [budget, len); slices start at multiples of 4
-  // from the start of their side, the second side's start rounded down (row_of).
+  // from the start of their side, the second side's start rounded down.
   int c1 = (int)(((long long)n_cta * budget + len / 2) / len);
   c1 = c1 < 1 ? 1 : (c1 > n_cta - 1 ? n_cta - 1 : c1);
   const int a0 = budget & ~3;
@@ -387,6 +388,9 @@ Device this_device() {
 // rows of 8 K/V heads 77 us, 119 on two CTAs each).  Long lists go to 16 CTAs, as many as find room
 // for all of them at once: 131072 rows 23.4 us against 26.7 on eight, 65536 rows 18.8 against 20.5 (7
 // lists; 8 lists, for which there is no room, 35.4), but 32768 rows 17.9 against 16.4.
+// The host knows the table's width and not the lengths, so `cap` is the former: 32 lists of 4224 rows in a
+// table for 32768 rows take as long as in one that just fits (12.6 and 11.0 us, replayed), in one for 131072
+// rows they get eight CTAs of 1024 threads each, twice what the SMs hold at once, and take 38 us.
 int cluster_of(long long lists, long long cap, const Device& dev) {
   if (cap >= 65536 && lists <= dev.large) return kLargest;
   int cluster = 2;

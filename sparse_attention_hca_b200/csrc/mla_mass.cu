@@ -468,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         wait_free();
         if (!finish) {
           group_bar(1 + wg, 128);
-          col[in_cta] = sum;
+          col[in_cta] = sum;  // (without `low`: one fp32 rounding per warpgroup and piece)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.sum_ready);
           handed = true;
